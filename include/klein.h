@@ -411,6 +411,95 @@ int klein_op_gemm_nvfp4(const void* a, const void* a_sf, const float* a_g, const
 int klein_op_attention(const void* q, const void* k, const void* vt, int batch, int rows, int rows_pad,
                        void* out, long long out_ld, void* stream);
 
+/* ------------------------------------------------------------------ training ops
+ * What adapter training and fine-tuning of a block need besides its forward
+ * kernels ([blog] "Smaller GPUs, single files, and custom LoRA training"):
+ * a linear layer with its epilogue, and its gradients. Same conventions as
+ * above. Results do not depend on the order in which the GPU runs things: the
+ * same call gives the same bits. */
+
+#define KLEIN_ACT_NONE 0
+#define KLEIN_ACT_SILU 1  /* z / (1 + e^-z) */
+#define KLEIN_ACT_GELU 2  /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+
+/* out = residual + alpha * act(x w^T + bias).
+ *   x         device bf16 [m][k], row pitch x_ld >= k elements, a multiple of 8
+ *   w         device bf16 [n][k], row pitch w_ld >= k elements, a multiple of 8
+ *   bias      device float [n], or NULL
+ *   residual  device [m][n], row pitch residual_ld >= n, float if residual_f32
+ *             else bf16; or NULL. May be out itself (same address, pitch and
+ *             type: the layer then adds onto out); must not overlap it otherwise.
+ *   out       device [m][n], row pitch out_ld >= n, float if out_f32 else bf16
+ *   preact    device bf16 [m][n], row pitch preact_ld >= n, receives
+ *             x w^T + bias for klein_op_linear_backward; or NULL
+ * m, n, k >= 1, any value (only x_ld and w_ld must be multiples of 8; elements
+ * between k and the pitch are never used). Sums in fp32, rounded once on output.
+ * x, w: 16-byte aligned; bias, float residual, float out: 4-byte; the others
+ * 2-byte (16-byte alignment and pitches that are multiples of 4 are faster).
+ * ws: klein_linear_workspace_size(m, n, k) bytes, 16-byte aligned (NULL if 0);
+ * one call at a time. Errors: KLEIN_ERR_INVALID_ARG, KLEIN_ERR_SHAPE,
+ * KLEIN_ERR_ALIGN, KLEIN_ERR_WORKSPACE. */
+typedef struct {
+  int m, n, k;
+  const void* x;
+  long long x_ld;
+  const void* w;
+  long long w_ld;
+  const float* bias;
+  const void* residual;
+  long long residual_ld;
+  int residual_f32;
+  int act;
+  float alpha;
+  void* out;
+  long long out_ld;
+  int out_f32;
+  void* preact;
+  long long preact_ld;
+} klein_linear_args;
+
+size_t klein_linear_workspace_size(int m, int n, int k);
+int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of klein_op_linear from dout = dL/dout:
+ *   dz = alpha * dout * act'(preact);  dx = dz w;  dw = dz^T x;  dbias = column sums of dz
+ * (the residual's gradient is dout). dz is rounded to bf16, the operand type,
+ * for the two products; dbias sums it unrounded.
+ *   dout    device [m][n], row pitch dout_ld >= n, float if dout_f32 else bf16
+ *   x, w    as in the forward call (x is read only for dw, w only for dx; the
+ *           one not needed may be NULL)
+ *   preact  as the forward call wrote it; may be NULL if act is KLEIN_ACT_NONE
+ *   dx      device [m][k], row pitch dx_ld >= k, float if dx_f32 else bf16, or NULL
+ *   dw      device [n][k], row pitch dw_ld >= k, float if dw_f32 else bf16, or NULL
+ *   dbias   device float [n], or NULL
+ * At least one of dx, dw, dbias. Outputs must not overlap any input.
+ * ws: klein_linear_backward_workspace_size(m, n, k) bytes, 16-byte aligned;
+ * one call at a time. Alignment and errors as for klein_op_linear. */
+typedef struct {
+  int m, n, k;
+  const void* dout;
+  long long dout_ld;
+  int dout_f32;
+  const void* x;
+  long long x_ld;
+  const void* w;
+  long long w_ld;
+  const void* preact;
+  long long preact_ld;
+  int act;
+  float alpha;
+  void* dx;
+  long long dx_ld;
+  int dx_f32;
+  void* dw;
+  long long dw_ld;
+  int dw_f32;
+  float* dbias;
+} klein_linear_grad_args;
+
+size_t klein_linear_backward_workspace_size(int m, int n, int k);
+int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t ws_bytes, void* stream);
+
 /* Per-stage, per-stream modulation and the final (shift, scale) of one
  * denoiser call (see klein_stack_forward). mod_out: device float
  * [2][3][3][3072]; final_out: device float [2][3072]; ws: device,

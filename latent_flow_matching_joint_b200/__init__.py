@@ -62,6 +62,21 @@ class KleinModelDesc(Structure):
                 ("final_mod", c_void_p), ("final_out", c_void_p), ("txt_in", c_void_p)]
 
 
+class KleinLinearArgs(Structure):
+    _fields_ = [("m", c_int), ("n", c_int), ("k", c_int), ("x", c_void_p), ("x_ld", c_longlong), ("w", c_void_p),
+                ("w_ld", c_longlong), ("bias", c_void_p), ("residual", c_void_p), ("residual_ld", c_longlong),
+                ("residual_f32", c_int), ("act", c_int), ("alpha", c_float), ("out", c_void_p),
+                ("out_ld", c_longlong), ("out_f32", c_int), ("preact", c_void_p), ("preact_ld", c_longlong)]
+
+
+class KleinLinearGradArgs(Structure):
+    _fields_ = [("m", c_int), ("n", c_int), ("k", c_int), ("dout", c_void_p), ("dout_ld", c_longlong),
+                ("dout_f32", c_int), ("x", c_void_p), ("x_ld", c_longlong), ("w", c_void_p), ("w_ld", c_longlong),
+                ("preact", c_void_p), ("preact_ld", c_longlong), ("act", c_int), ("alpha", c_float),
+                ("dx", c_void_p), ("dx_ld", c_longlong), ("dx_f32", c_int), ("dw", c_void_p),
+                ("dw_ld", c_longlong), ("dw_f32", c_int), ("dbias", c_void_p)]
+
+
 _SIGS = {
     "klein_last_error": (ctypes.c_char_p, []),
     "klein_version": (c_int, []),
@@ -107,6 +122,10 @@ _SIGS = {
                                      c_void_p, c_void_p, c_void_p, c_void_p]),
     "klein_op_gemm_nvfp4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                     c_int, c_void_p]),
+    "klein_linear_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "klein_op_linear": (c_int, [POINTER(KleinLinearArgs), c_void_p, c_size_t, c_void_p]),
+    "klein_linear_backward_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "klein_op_linear_backward": (c_int, [POINTER(KleinLinearGradArgs), c_void_p, c_size_t, c_void_p]),
     "klein_op_time_mod": (c_int, [c_void_p, c_float, c_float, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
                                   c_void_p]),
 }
@@ -429,3 +448,139 @@ def klein_op_time_mod(model: KleinModel, sigma: float, sigma_next: float, with_r
                       stream=None):
     _check(lib.klein_op_time_mod(model.handle, sigma, sigma_next, int(with_ref), _ptr(mod_out), _ptr(final_out),
                                  _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ training ops
+# These take any torch layout the C functions can, so they look at each
+# tensor before its address leaves Python: a wrong type, shape, stride or
+# device raises KleinError and nothing is enqueued. The work goes to the
+# tensors' device, on its current stream unless `stream` names another.
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _refuse(code: int, msg: str):
+    raise KleinError(code, msg)
+
+
+def _same_device(device, tensors):
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            _refuse(-1, f"{name} is on {t.device}, not on {device}")
+
+
+def _run_on(device, call, stream):
+    """call(stream handle) with `device` current."""
+    import torch
+    if device.type != "cuda":
+        _refuse(-1, f"tensors on {device}: CUDA tensors needed")
+    if device.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream(stream)))
+
+
+def _matrix(name, t, shape, types):
+    """Row pitch of a 2-D tensor with unit column stride."""
+    if t.dtype not in types:
+        _refuse(-1, f"{name} has type {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        _refuse(-2, f"{name} is not contiguous along its last dimension")
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8  # the pitch of a single row is never used
+
+
+def _vector(name, t, n, dtype):
+    if t.dtype != dtype:
+        _refuse(-1, f"{name} has type {t.dtype}, not {dtype}")
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        _refuse(-2, f"{name} is not a contiguous vector of {n}")
+
+
+def _workspace(ws):
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        _refuse(-2, "the workspace is not contiguous")
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        _refuse(-1, f"unknown activation {act!r}")
+    return ACTIVATIONS[act]
+
+
+def klein_linear_workspace_size(m: int, n: int, k: int) -> int:
+    return lib.klein_linear_workspace_size(m, n, k)
+
+
+def klein_op_linear(x, w, out, ws=None, bias=None, residual=None, act: str = "none", alpha: float = 1.0,
+                    preact=None, stream=None):
+    """out = residual + alpha * act(x w^T + bias): x bf16 [m, k], w bf16 [n, k], bias
+    float32 [n], residual and out bf16 or float32 [m, n] (residual may be out),
+    preact bf16 [m, n] receives x w^T + bias. act: "none", "silu", "gelu" (tanh
+    form). ws: klein_linear_workspace_size(m, n, k) bytes."""
+    import torch
+    bf16, both = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+    if x.dim() != 2 or w.dim() != 2:
+        _refuse(-2, "x and w must be matrices")
+    (m, k), n = x.shape, w.shape[0]
+    a = KleinLinearArgs()
+    a.m, a.n, a.k = m, n, k
+    a.x, a.x_ld = x.data_ptr(), _matrix("x", x, (m, k), bf16)
+    a.w, a.w_ld = w.data_ptr(), _matrix("w", w, (n, k), bf16)
+    a.out, a.out_ld, a.out_f32 = out.data_ptr(), _matrix("out", out, (m, n), both), out.dtype == torch.float32
+    if bias is not None:
+        _vector("bias", bias, n, torch.float32)
+        a.bias = bias.data_ptr()
+    if residual is not None:
+        a.residual, a.residual_ld = residual.data_ptr(), _matrix("residual", residual, (m, n), both)
+        a.residual_f32 = residual.dtype == torch.float32
+    if preact is not None:
+        a.preact, a.preact_ld = preact.data_ptr(), _matrix("preact", preact, (m, n), bf16)
+    a.act, a.alpha = _activation(act), alpha
+    _same_device(x.device, (("w", w), ("out", out), ("ws", ws), ("bias", bias), ("residual", residual),
+                            ("preact", preact)))
+    ws_ptr, ws_bytes = _workspace(ws)
+    _run_on(x.device, lambda s: lib.klein_op_linear(ctypes.byref(a), ws_ptr, ws_bytes, s), stream)
+
+
+def klein_linear_backward_workspace_size(m: int, n: int, k: int) -> int:
+    return lib.klein_linear_backward_workspace_size(m, n, k)
+
+
+def klein_op_linear_backward(dout, x, w, ws, dx=None, dw=None, dbias=None, preact=None, act: str = "none",
+                             alpha: float = 1.0, stream=None):
+    """Gradients of klein_op_linear: with dz = alpha * dout * act'(preact), dx = dz w,
+    dw = dz^T x, dbias = dz summed over rows, each written if given. dout, dx and
+    dw bf16 or float32, dbias float32. ws: klein_linear_backward_workspace_size
+    (m, n, k) bytes."""
+    import torch
+    bf16, both = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+    if x.dim() != 2 or w.dim() != 2:
+        _refuse(-2, "x and w must be matrices")
+    (m, k), n = x.shape, w.shape[0]
+    a = KleinLinearGradArgs()
+    a.m, a.n, a.k = m, n, k
+    a.dout, a.dout_ld = dout.data_ptr(), _matrix("dout", dout, (m, n), both)
+    a.dout_f32 = dout.dtype == torch.float32
+    a.x, a.x_ld = x.data_ptr(), _matrix("x", x, (m, k), bf16)
+    a.w, a.w_ld = w.data_ptr(), _matrix("w", w, (n, k), bf16)
+    if preact is not None:
+        a.preact, a.preact_ld = preact.data_ptr(), _matrix("preact", preact, (m, n), bf16)
+    if dx is not None:
+        a.dx, a.dx_ld, a.dx_f32 = dx.data_ptr(), _matrix("dx", dx, (m, k), both), dx.dtype == torch.float32
+    if dw is not None:
+        a.dw, a.dw_ld, a.dw_f32 = dw.data_ptr(), _matrix("dw", dw, (n, k), both), dw.dtype == torch.float32
+    if dbias is not None:
+        _vector("dbias", dbias, n, torch.float32)
+        a.dbias = dbias.data_ptr()
+    a.act, a.alpha = _activation(act), alpha
+    _same_device(x.device, (("dout", dout), ("w", w), ("ws", ws), ("preact", preact), ("dx", dx), ("dw", dw),
+                            ("dbias", dbias)))
+    ws_ptr, ws_bytes = _workspace(ws)
+    _run_on(x.device, lambda s: lib.klein_op_linear_backward(ctypes.byref(a), ws_ptr, ws_bytes, s), stream)

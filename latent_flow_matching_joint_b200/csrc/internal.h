@@ -116,6 +116,75 @@ struct AttnArgs {
 // Returns 0, -1 on a launch error, -2 if a tensor map cannot be encoded.
 int launch_attention(const AttnArgs& args, cudaStream_t stream);
 
+// ------------------------------------------------------------------ linear layer
+
+enum ActKind : int { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+
+// Epilogue of an m x n product: z = acc + bias; out = res + alpha * act(z); z kept if asked for.
+struct LinEpi {
+  int m, n;
+  void* out;
+  long long out_ld;
+  const float* bias;  // [n] or null
+  const void* res;    // [m][res_ld] or null; may be the output itself
+  long long res_ld;
+  __nv_bfloat16* z;   // [m][z_ld] or null
+  long long z_ld;
+  float alpha;
+  int act;
+  int out_f32, res_f32;             // element types: fp32, else bf16
+  int out_vec, res_vec, z_vec;      // four columns may be accessed at once (address and pitch allow it)
+};
+
+struct LinGemmArgs {
+  int m_tiles, n_tiles, k_blocks, splits;
+  int n_fastest;       // visit tiles N-fastest instead of M-fastest
+  float* partial;      // splits > 1: [splits][m][partial_ld] partial sums
+  long long partial_ld;
+  LinEpi epi;
+};
+
+// One operand of C[m][n] = sum_k A(m, k) B(n, k): element (i, k) at data[i * ld + k],
+// or at data[k * ld + i] when mn_major. 16-byte aligned, ld a multiple of 8.
+struct LinOperand {
+  const void* data;
+  long long ld;
+  int mn_major;
+};
+
+struct LinPlan {
+  int pair, splits;
+  long long partial_ld;
+  size_t partial_bytes;  // workspace for partial sums, 0 without a split
+};
+LinPlan plan_linear(long long m, long long n, long long k);
+
+// The product and its epilogue (one or two launches). A row-contiguous only
+// together with B. Returns 0, -1 (launch) or -2 (tensor map).
+int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const LinEpi& epi, float* partial,
+                       cudaStream_t stream);
+// The same for at most 4 rows of k-contiguous operands, without tensor cores.
+constexpr int kLinMaxRows = 4;
+int launch_linear_rows(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
+                       const LinEpi& epi, cudaStream_t stream);
+
+struct LinDzArgs {
+  long long m;
+  int n, slab;          // slab: rows per block (lin_dz_slab)
+  const void* dout;
+  long long dout_ld;
+  int dout_f32, dout_vec;
+  const __nv_bfloat16* z;
+  long long z_ld;
+  int z_vec, act;
+  float alpha;
+  __nv_bfloat16* dz;    // [m][dz_ld], dz_ld a multiple of 8; or null
+  long long dz_ld;
+  float* col_part;      // [slabs][n] column sums of the slabs, or null
+};
+int lin_dz_slab(long long m, int n);
+int launch_linear_dz(const LinDzArgs& a, float* dbias, cudaStream_t stream);
+
 // ------------------------------------------------------------------ memory-bound kernels
 
 int launch_modln(const float* x, long long x_bstride, int x_row0, __nv_bfloat16* h, int batch, int rows,

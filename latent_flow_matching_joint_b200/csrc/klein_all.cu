@@ -5,5 +5,6 @@
 #include "gemm.cu"
 #include "attention.cu"
 #include "nvfp4.cu"
+#include "linear.cu"
 #include "klein_capi.cu"
 #include "static_ws.cu"

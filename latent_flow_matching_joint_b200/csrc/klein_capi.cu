@@ -1140,4 +1140,186 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
   return KLEIN_OK;
 }
 
+// ------------------------------------------------------------------ linear layer
+
+// Whether four columns at a time may be accessed: the address and the pitch
+// keep every group of four on its own size's boundary.
+static int vec4_ok(const void* p, long long ld, int f32) {
+  return (reinterpret_cast<uintptr_t>(p) & (f32 ? 15u : 7u)) == 0 && (ld % 4) == 0;
+}
+
+static bool element_aligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0; }
+
+static int check_linear_sizes(int m, int n, int k) {
+  if (m < 1 || n < 1 || k < 1) return fail(KLEIN_ERR_SHAPE, "need m, n, k >= 1");
+  // tile counts and grids are int
+  auto tiles = [](long long a, long long b) { return ((a + 127) / 128) * ((b + 127) / 128); };
+  if (tiles(m, n) > (1 << 26) || tiles(m, k) > (1 << 26) || tiles(n, k) > (1 << 26))
+    return fail(KLEIN_ERR_SHAPE, "matrix too large");
+  return KLEIN_OK;
+}
+
+static int check_operand(const char* name, const void* p, long long ld, int cols) {
+  if (!p) return fail(KLEIN_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p) || (ld % 8) != 0) return fail(KLEIN_ERR_ALIGN, "%s needs a 16-byte aligned address and a row pitch that is a multiple of 8", name);
+  if (ld < cols || ld >= (1ll << 38)) return fail(KLEIN_ERR_SHAPE, "bad row pitch of %s", name);
+  return KLEIN_OK;
+}
+
+static int check_matrix(const char* name, const void* p, long long ld, int cols, int f32) {
+  if (!element_aligned(p, f32)) return fail(KLEIN_ERR_ALIGN, "%s is not aligned to its element", name);
+  if (ld < cols || ld >= (1ll << 38)) return fail(KLEIN_ERR_SHAPE, "bad row pitch of %s", name);
+  return KLEIN_OK;
+}
+
+size_t klein_linear_workspace_size(int m, int n, int k) {
+  if (m < 1 || n < 1 || k < 1 || m <= kLinMaxRows) return 0;
+  return plan_linear(m, n, k).partial_bytes;
+}
+
+int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a || !a->out) return fail(KLEIN_ERR_INVALID_ARG, "NULL argument");
+  int rc;
+  if ((rc = check_linear_sizes(a->m, a->n, a->k)) || (rc = check_operand("x", a->x, a->x_ld, a->k)) ||
+      (rc = check_operand("w", a->w, a->w_ld, a->k)) || (rc = check_matrix("out", a->out, a->out_ld, a->n, a->out_f32)))
+    return rc;
+  if (a->residual && (rc = check_matrix("residual", a->residual, a->residual_ld, a->n, a->residual_f32))) return rc;
+  if (a->preact && (rc = check_matrix("preact", a->preact, a->preact_ld, a->n, 0))) return rc;
+  if (a->bias && !element_aligned(a->bias, 1)) return fail(KLEIN_ERR_ALIGN, "bias is not aligned to its element");
+  if (a->act < KLEIN_ACT_NONE || a->act > KLEIN_ACT_GELU) return fail(KLEIN_ERR_INVALID_ARG, "unknown activation");
+  if (a->residual == a->out && (a->residual_ld != a->out_ld || !a->residual_f32 != !a->out_f32))
+    return fail(KLEIN_ERR_INVALID_ARG, "out is the residual, with another pitch or type");
+  const size_t need = klein_linear_workspace_size(a->m, a->n, a->k);
+  if (ws_bytes < need || (need && !ws)) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", need);
+  if (need && !aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  LinEpi e{};
+  e.m = a->m;
+  e.n = a->n;
+  e.out = a->out;
+  e.out_ld = a->out_ld;
+  e.out_f32 = a->out_f32 != 0;
+  e.out_vec = vec4_ok(a->out, a->out_ld, e.out_f32);
+  e.bias = a->bias;
+  e.res = a->residual;
+  e.res_ld = a->residual_ld;
+  e.res_f32 = a->residual_f32 != 0;
+  e.res_vec = vec4_ok(a->residual, a->residual_ld, e.res_f32);
+  e.z = static_cast<__nv_bfloat16*>(a->preact);
+  e.z_ld = a->preact_ld;
+  e.z_vec = vec4_ok(a->preact, a->preact_ld, 0);
+  e.alpha = a->alpha;
+  e.act = a->act;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->m <= kLinMaxRows)
+    rc = launch_linear_rows(static_cast<const __nv_bfloat16*>(a->x), a->x_ld, static_cast<const __nv_bfloat16*>(a->w),
+                            a->w_ld, a->k, e, s);
+  else
+    rc = launch_linear_gemm({a->x, a->x_ld, 0}, {a->w, a->w_ld, 0}, a->k, e, static_cast<float*>(ws), s);
+  if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  if (rc) return cuda_fail("linear launch");
+  return KLEIN_OK;
+}
+
+// Workspace of klein_op_linear_backward: dz, the slabs' column sums, and the
+// partial sums of the larger of the two split products (they run one after
+// the other).
+struct LinearGradWs {
+  size_t dz, col_part, partial, bytes;
+};
+
+static LinearGradWs carve_linear_grad(int m, int n, int k) {
+  LinearGradWs w{};
+  const size_t slab = lin_dz_slab(m, n);
+  const size_t dx = plan_linear(m, k, n).partial_bytes, dw = plan_linear(n, k, m).partial_bytes;
+  w.dz = 0;
+  w.col_part = w.dz + align256((size_t)m * (((size_t)n + 7) / 8 * 8) * 2);
+  w.partial = w.col_part + align256(((size_t)m + slab - 1) / slab * n * 4);
+  w.bytes = w.partial + align256(dx > dw ? dx : dw);
+  return w;
+}
+
+size_t klein_linear_backward_workspace_size(int m, int n, int k) {
+  if (m < 1 || n < 1 || k < 1) return 0;
+  return carve_linear_grad(m, n, k).bytes;
+}
+
+int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t ws_bytes, void* stream) {
+  if (!a || !a->dout) return fail(KLEIN_ERR_INVALID_ARG, "NULL argument");
+  if (!a->dx && !a->dw && !a->dbias) return fail(KLEIN_ERR_INVALID_ARG, "no gradient asked for");
+  int rc;
+  if ((rc = check_linear_sizes(a->m, a->n, a->k)) ||
+      (rc = check_matrix("dout", a->dout, a->dout_ld, a->n, a->dout_f32)))
+    return rc;
+  if (a->act < KLEIN_ACT_NONE || a->act > KLEIN_ACT_GELU) return fail(KLEIN_ERR_INVALID_ARG, "unknown activation");
+  if (a->act != KLEIN_ACT_NONE) {
+    if (!a->preact) return fail(KLEIN_ERR_INVALID_ARG, "preact is NULL");
+    if ((rc = check_matrix("preact", a->preact, a->preact_ld, a->n, 0))) return rc;
+  }
+  if (a->dx && ((rc = check_operand("w", a->w, a->w_ld, a->k)) || (rc = check_matrix("dx", a->dx, a->dx_ld, a->k, a->dx_f32))))
+    return rc;
+  if (a->dw && ((rc = check_operand("x", a->x, a->x_ld, a->k)) || (rc = check_matrix("dw", a->dw, a->dw_ld, a->k, a->dw_f32))))
+    return rc;
+  if (a->dbias && !element_aligned(a->dbias, 1)) return fail(KLEIN_ERR_ALIGN, "dbias is not aligned to its element");
+  const LinearGradWs w = carve_linear_grad(a->m, a->n, a->k);
+  if (!ws || ws_bytes < w.bytes) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", w.bytes);
+  if (!aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  // dout itself is the products' operand when nothing but alpha separates it
+  // from dz (alpha then goes into their epilogues) and TMA can read it.
+  const bool direct = a->act == KLEIN_ACT_NONE && !a->dout_f32 && aligned16(a->dout) && (a->dout_ld % 8) == 0;
+  const bool products = a->dx || a->dw;
+  LinOperand dz{a->dout, a->dout_ld, 0};
+  if ((products && !direct) || a->dbias) {
+    LinDzArgs d{};
+    d.m = a->m;
+    d.n = a->n;
+    d.slab = lin_dz_slab(a->m, a->n);
+    d.dout = a->dout;
+    d.dout_ld = a->dout_ld;
+    d.dout_f32 = a->dout_f32 != 0;
+    d.dout_vec = aligned16(a->dout) && (a->dout_ld % (d.dout_f32 ? 4 : 8)) == 0;
+    d.z = static_cast<const __nv_bfloat16*>(a->preact);
+    d.z_ld = a->preact_ld;
+    d.z_vec = aligned16(a->preact) && (a->preact_ld % 8) == 0;
+    d.act = a->act;
+    d.alpha = a->alpha;
+    if (products && !direct) {
+      d.dz = reinterpret_cast<__nv_bfloat16*>(base + w.dz);
+      d.dz_ld = ((long long)a->n + 7) / 8 * 8;
+      dz = {d.dz, d.dz_ld, 0};
+    }
+    d.col_part = a->dbias ? reinterpret_cast<float*>(base + w.col_part) : nullptr;
+    if (launch_linear_dz(d, a->dbias, s)) return cuda_fail("linear gradient launch");
+  }
+  LinEpi e{};
+  e.alpha = direct ? a->alpha : 1.0f;
+  e.act = kActNone;
+  float* partial = reinterpret_cast<float*>(base + w.partial);
+  if (a->dx) {
+    e.m = a->m;
+    e.n = a->k;
+    e.out = a->dx;
+    e.out_ld = a->dx_ld;
+    e.out_f32 = a->dx_f32 != 0;
+    e.out_vec = vec4_ok(a->dx, a->dx_ld, e.out_f32);
+    rc = launch_linear_gemm(dz, {a->w, a->w_ld, 1}, a->n, e, partial, s);
+    if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    if (rc) return cuda_fail("linear gradient launch");
+  }
+  if (a->dw) {
+    e.m = a->n;
+    e.n = a->k;
+    e.out = a->dw;
+    e.out_ld = a->dw_ld;
+    e.out_f32 = a->dw_f32 != 0;
+    e.out_vec = vec4_ok(a->dw, a->dw_ld, e.out_f32);
+    dz.mn_major = 1;
+    rc = launch_linear_gemm(dz, {a->x, a->x_ld, 1}, a->m, e, partial, s);
+    if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    if (rc) return cuda_fail("linear gradient launch");
+  }
+  return KLEIN_OK;
+}
+
 }  // extern "C"
