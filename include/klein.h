@@ -414,9 +414,56 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
 /* ------------------------------------------------------------------ training ops
  * What adapter training and fine-tuning of a block need besides its forward
  * kernels ([blog] "Smaller GPUs, single files, and custom LoRA training"):
- * a linear layer with its epilogue, and its gradients. Same conventions as
+ * attention with its row statistics, a linear layer with its epilogue, and
+ * the gradients of both. Same conventions as
  * above. Results do not depend on the order in which the GPU runs things: the
  * same call gives the same bits. */
+
+/* A bf16 tensor [batch][heads][rows][128] in any layout with contiguous heads'
+ * vectors: the distance between neighbours along each axis, in elements.
+ * Strides are multiples of 8, at least 128 (not looked at along an axis of
+ * length one); data is 16-byte aligned. A [batch][rows][heads][128] tensor,
+ * or q, k and v inside one projection's output, need no copy. */
+typedef struct {
+  void* data;
+  long long batch_stride, head_stride, row_stride;
+} klein_heads;
+
+/* rows is the length of the sequence that queries, keys and values share;
+ * query head h reads key head h / (heads / kv_heads), heads a multiple of
+ * kv_heads. scale > 0 multiplies q . k (1 / sqrt(128) in the denoiser).
+ * txt_len: NULL, then every row attends to every row, as in the denoiser
+ * (n_txt is not looked at); or device int [batch], the number of text tokens of
+ * each item (clamped to [0, n_txt]): its rows [txt_len, n_txt) are padding.
+ * Padding neither attends nor is attended to, whatever its rows hold (NaN
+ * included): their out and gradients are 0, their lse -infinity. */
+typedef struct {
+  int batch, heads, kv_heads, rows;
+  int n_txt;
+  const int* txt_len;
+  float scale;
+} klein_attention_shape;
+
+/* out = softmax(scale q k^T) v; lse: device float [batch][heads][rows], the
+ * natural logarithm of each row's sum of exp(scale q . k), which the backward
+ * pass needs. Scores, softmax and sums in fp32, probabilities rounded to bf16
+ * for their product with v. out must not overlap the inputs or itself.
+ * Errors: KLEIN_ERR_INVALID_ARG, KLEIN_ERR_SHAPE, KLEIN_ERR_ALIGN. */
+int klein_op_attention_forward(const klein_attention_shape* shape, const klein_heads* q, const klein_heads* k,
+                               const klein_heads* v, const klein_heads* out, float* lse, void* stream);
+
+/* Gradients of klein_op_attention_forward from dout = dL/dout; out and lse as it
+ * wrote them. dk and dv sum over the query heads that share the key head.
+ * Probabilities are recomputed from lse; they and the scores' gradients are
+ * rounded to bf16 for their products, every sum is fp32. dq, dk, dv must not
+ * overlap the inputs, one another or themselves. ws:
+ * klein_attention_backward_workspace_size bytes (n_txt = 0 without txt_len),
+ * 16-byte aligned; one call at a time. Errors as above, KLEIN_ERR_WORKSPACE. */
+size_t klein_attention_backward_workspace_size(int batch, int heads, int rows, int n_txt);
+int klein_op_attention_backward(const klein_attention_shape* shape, const klein_heads* q, const klein_heads* k,
+                                const klein_heads* v, const klein_heads* out, const float* lse,
+                                const klein_heads* dout, const klein_heads* dq, const klein_heads* dk,
+                                const klein_heads* dv, void* ws, size_t ws_bytes, void* stream);
 
 #define KLEIN_ACT_NONE 0
 #define KLEIN_ACT_SILU 1  /* z / (1 + e^-z) */

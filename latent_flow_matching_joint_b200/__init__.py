@@ -62,6 +62,16 @@ class KleinModelDesc(Structure):
                 ("final_mod", c_void_p), ("final_out", c_void_p), ("txt_in", c_void_p)]
 
 
+class KleinHeads(Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", c_longlong), ("head_stride", c_longlong),
+                ("row_stride", c_longlong)]
+
+
+class KleinAttentionShape(Structure):
+    _fields_ = [("batch", c_int), ("heads", c_int), ("kv_heads", c_int), ("rows", c_int), ("n_txt", c_int),
+                ("txt_len", c_void_p), ("scale", c_float)]
+
+
 class KleinLinearArgs(Structure):
     _fields_ = [("m", c_int), ("n", c_int), ("k", c_int), ("x", c_void_p), ("x_ld", c_longlong), ("w", c_void_p),
                 ("w_ld", c_longlong), ("bias", c_void_p), ("residual", c_void_p), ("residual_ld", c_longlong),
@@ -122,6 +132,11 @@ _SIGS = {
                                      c_void_p, c_void_p, c_void_p, c_void_p]),
     "klein_op_gemm_nvfp4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                     c_int, c_void_p]),
+    "klein_op_attention_forward": (c_int, [POINTER(KleinAttentionShape)] + [POINTER(KleinHeads)] * 4
+                                   + [c_void_p, c_void_p]),
+    "klein_attention_backward_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "klein_op_attention_backward": (c_int, [POINTER(KleinAttentionShape)] + [POINTER(KleinHeads)] * 4 + [c_void_p]
+                                    + [POINTER(KleinHeads)] * 4 + [c_void_p, c_size_t, c_void_p]),
     "klein_linear_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "klein_op_linear": (c_int, [POINTER(KleinLinearArgs), c_void_p, c_size_t, c_void_p]),
     "klein_linear_backward_workspace_size": (c_size_t, [c_int, c_int, c_int]),
@@ -479,6 +494,75 @@ def _run_on(device, call, stream):
     else:
         with torch.cuda.device(device):
             _check(call(_stream(stream)))
+
+
+def _heads(name, t, shape):
+    import torch
+    if t.dtype != torch.bfloat16:
+        _refuse(-1, f"{name} has type {t.dtype}, not bfloat16")
+    if tuple(t.shape) != shape:
+        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    sb, sh, sr, sd = t.stride()
+    if sd != 1:
+        _refuse(-2, f"{name} is not contiguous along its last dimension")
+    return ctypes.byref(KleinHeads(t.data_ptr(), sb, sh, sr))
+
+
+def _attention_shape(q, k, n_txt, txt_len, scale):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        _refuse(-2, "q and k must be [batch, heads, rows, 128]")
+    batch, heads, rows, _ = q.shape
+    s = KleinAttentionShape(batch, heads, k.shape[1], rows, n_txt, None, HEAD_DIM ** -0.5 if scale is None else scale)
+    if txt_len is not None:
+        _vector("txt_len", txt_len, batch, torch.int32)
+        s.txt_len = txt_len.data_ptr()
+    return s, (batch, heads, rows, HEAD_DIM), (batch, k.shape[1], rows, HEAD_DIM)
+
+
+def _statistics(lse, shape):
+    import torch
+    if lse.dtype != torch.float32:
+        _refuse(-1, f"lse has type {lse.dtype}, not float32")
+    if tuple(lse.shape) != shape or not lse.is_contiguous():
+        _refuse(-2, f"lse is not a contiguous {shape} tensor")
+    return _ptr(lse)
+
+
+def klein_op_attention_forward(q, k, v, out, lse, n_txt: int = 0, txt_len=None, scale: float | None = None,
+                               stream=None):
+    """out = softmax(scale q k^T) v and lse, the log of each row's sum of
+    exponentials, for klein_op_attention_backward. q and out bf16 [batch, heads,
+    rows, 128], k and v bf16 [batch, kv_heads, rows, 128], any strides with a
+    contiguous last dimension; lse float32 [batch, heads, rows]. With txt_len
+    (int32 [batch] on the device) rows [txt_len, n_txt) of an item are padding.
+    scale: 1/sqrt(128) unless given."""
+    shape, qs, ks = _attention_shape(q, k, n_txt, txt_len, scale)
+    args = (_heads("q", q, qs), _heads("k", k, ks), _heads("v", v, ks), _heads("out", out, qs),
+            _statistics(lse, qs[:3]))
+    _same_device(q.device, (("k", k), ("v", v), ("out", out), ("lse", lse), ("txt_len", txt_len)))
+    _run_on(q.device, lambda s: lib.klein_op_attention_forward(ctypes.byref(shape), *args, s), stream)
+
+
+def klein_attention_backward_workspace_size(batch: int, heads: int, rows: int, n_txt: int = 0) -> int:
+    return lib.klein_attention_backward_workspace_size(batch, heads, rows, n_txt)
+
+
+def klein_op_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, ws, n_txt: int = 0, txt_len=None,
+                                scale: float | None = None, stream=None):
+    """dq, dk, dv from dout, with q, k, v, out, lse and the lengths as
+    klein_op_attention_forward had and wrote them; dq and dout like q, dk and dv
+    like k. ws: klein_attention_backward_workspace_size(batch, heads, rows, n_txt)
+    bytes."""
+    shape, qs, ks = _attention_shape(q, k, n_txt, txt_len, scale)
+    inputs = (_heads("q", q, qs), _heads("k", k, ks), _heads("v", v, ks), _heads("out", out, qs),
+              _statistics(lse, qs[:3]), _heads("dout", dout, qs))
+    outputs = (_heads("dq", dq, qs), _heads("dk", dk, ks), _heads("dv", dv, ks))
+    _same_device(q.device, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dq", dq), ("dk", dk),
+                            ("dv", dv), ("ws", ws), ("txt_len", txt_len)))
+    ws_ptr, ws_bytes = _workspace(ws)
+    _run_on(q.device, lambda s: lib.klein_op_attention_backward(ctypes.byref(shape), *inputs, *outputs, ws_ptr,
+                                                                 ws_bytes, s), stream)
 
 
 def _matrix(name, t, shape, types):

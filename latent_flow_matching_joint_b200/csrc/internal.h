@@ -19,6 +19,9 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t out
 // 3-D bf16 tensor map over [d2][d1][d0] with byte strides s1 (d1) and s2 (d2).
 int make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                 uint64_t s2, uint32_t box0, uint32_t box1, int bytes1 = 0);
+// 4-D bf16 tensor map over [d3][d2][d1][d0] with byte strides s1..s3; box = box0 x box1 x 1 x 1.
+int make_map_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
+                uint64_t s2, uint64_t s3, uint32_t box0, uint32_t box1);
 // 2-D map of 32-bit words [outer][inner], no swizzle (dense boxes).
 int make_map_2d_u32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                     uint32_t box_inner, uint32_t box_outer);
@@ -115,6 +118,32 @@ struct AttnArgs {
 // Builds the operand tensor maps and launches the attention kernel.
 // Returns 0, -1 on a launch error, -2 if a tensor map cannot be encoded.
 int launch_attention(const AttnArgs& args, cudaStream_t stream);
+
+// ------------------------------------------------------------------ attention for training
+
+// bf16 [batch][heads][rows][128] by its strides in elements.
+struct HeadsView {
+  void* data;
+  long long batch_stride, head_stride, row_stride;
+};
+
+struct AttnTrainArgs {
+  int batch, heads, kv_heads, rows;
+  int n_txt;           // rows [0, n_txt) have a length per item; 0 when txt_len is null
+  int slots;           // attn_slots(rows, n_txt)
+  const int* txt_len;  // device [batch], or null: every row takes part
+  float scale, scale_log2;
+  HeadsView q, k, v, out;
+  float* lse;          // [batch][heads][rows]
+  // backward
+  HeadsView dout, dq, dk, dv;
+  float* stats;        // [batch][heads][slots][2][128]
+};
+inline long long attn_slots(long long rows, long long n_txt) { return (n_txt + 127) / 128 + (rows - n_txt + 127) / 128; }
+
+// Return 0, -1 on a launch error, -2 if a tensor map cannot be encoded.
+int launch_attention_train(const AttnTrainArgs& args, cudaStream_t stream);
+int launch_attention_backward(const AttnTrainArgs& args, cudaStream_t stream);
 
 // ------------------------------------------------------------------ linear layer
 

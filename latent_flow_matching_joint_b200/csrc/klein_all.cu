@@ -4,6 +4,7 @@
 #include "kernels_mem.cu"
 #include "gemm.cu"
 #include "attention.cu"
+#include "attention_train.cu"
 #include "nvfp4.cu"
 #include "linear.cu"
 #include "klein_capi.cu"

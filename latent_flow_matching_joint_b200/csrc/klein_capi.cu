@@ -144,6 +144,19 @@ int make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, ui
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
+int make_map_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
+                uint64_t s2, uint64_t s3, uint32_t box0, uint32_t box1) {
+  if (get_encode()) return -1;
+  cuuint64_t dims[4] = {d0, d1, d2, d3};
+  cuuint64_t strides[3] = {s1, s2, s3};
+  cuuint32_t box[4] = {box0, box1, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 // ------------------------------------------------------------------ workspace
 
 static inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1140,6 +1153,118 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
   return KLEIN_OK;
 }
 
+// ------------------------------------------------------------------ attention for training
+
+static bool element_aligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0; }
+
+// Checks a [batch][heads][rows][128] view and returns it with usable strides
+// for axes of length one (they are never stepped along, but the tensor map
+// wants a multiple of 16 bytes). `written`: no element may have two indices.
+static int check_heads(const char* name, const klein_heads* t, int batch, int heads, int rows, bool written,
+                       HeadsView* v) {
+  if (!t || !t->data) return fail(KLEIN_ERR_INVALID_ARG, "%s is NULL", name);
+  *v = {t->data, t->batch_stride, t->head_stride, t->row_stride};
+  if (!aligned16(t->data)) return fail(KLEIN_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  const int n[3] = {batch, heads, rows};
+  long long* stride[3] = {&v->batch_stride, &v->head_stride, &v->row_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) *stride[i] = kHeadDim;
+    if (*stride[i] < kHeadDim || *stride[i] >= (1ll << 38))
+      return fail(KLEIN_ERR_SHAPE, "%s: strides must be at least 128 elements", name);
+    if (*stride[i] % 8) return fail(KLEIN_ERR_ALIGN, "%s: strides must be multiples of 8 elements", name);
+  }
+  if (written) {
+    // from the shortest stride to the longest, each step must clear what the shorter ones span
+    long long span = kHeadDim;
+    bool taken[3] = {batch == 1, heads == 1, rows == 1};
+    for (int pass = 0; pass < 3; ++pass) {
+      int at = -1;
+      for (int i = 0; i < 3; ++i)
+        if (!taken[i] && (at < 0 || *stride[i] < *stride[at])) at = i;
+      if (at < 0) break;
+      if (*stride[at] < span) return fail(KLEIN_ERR_SHAPE, "%s: rows overlap", name);
+      span += *stride[at] * (n[at] - 1);
+      taken[at] = true;
+    }
+  }
+  return KLEIN_OK;
+}
+
+static int check_attention_shape(const klein_attention_shape* s, AttnTrainArgs* a) {
+  if (!s) return fail(KLEIN_ERR_INVALID_ARG, "NULL argument");
+  if (s->batch < 1 || s->heads < 1 || s->kv_heads < 1 || s->rows < 1 || s->n_txt < 0 || s->n_txt > s->rows)
+    return fail(KLEIN_ERR_SHAPE, "need batch, heads, kv_heads, rows >= 1 and 0 <= n_txt <= rows");
+  if (s->heads % s->kv_heads) return fail(KLEIN_ERR_SHAPE, "heads must be a multiple of kv_heads");
+  if (!(s->scale > 0.f) || !(s->scale < INFINITY)) return fail(KLEIN_ERR_INVALID_ARG, "scale must be positive");
+  if (!element_aligned(s->txt_len, 1)) return fail(KLEIN_ERR_ALIGN, "txt_len is not aligned to its element");
+  a->batch = s->batch;
+  a->heads = s->heads;
+  a->kv_heads = s->kv_heads;
+  a->rows = s->rows;
+  a->txt_len = s->txt_len;
+  a->n_txt = s->txt_len ? s->n_txt : 0;  // without lengths the text is like every other row
+  a->scale = s->scale;
+  a->scale_log2 = static_cast<float>(1.4426950408889634 * s->scale);
+  const long long slots = attn_slots(a->rows, a->n_txt);
+  // launch grids: (slots, heads, batch), and one block per slot and head of either kind
+  if (a->rows > (1 << 30) || a->heads > 65535 || a->batch > 65535 ||
+      static_cast<double>(slots) * (a->heads + a->kv_heads) * a->batch > 2147483647.0)
+    return fail(KLEIN_ERR_SHAPE, "too many rows, heads or batch items");
+  a->slots = static_cast<int>(slots);
+  return KLEIN_OK;
+}
+
+int klein_op_attention_forward(const klein_attention_shape* shape, const klein_heads* q, const klein_heads* k,
+                               const klein_heads* v, const klein_heads* out, float* lse, void* stream) {
+  AttnTrainArgs a{};
+  int rc = check_attention_shape(shape, &a);
+  if (rc || (rc = check_heads("q", q, a.batch, a.heads, a.rows, false, &a.q)) ||
+      (rc = check_heads("k", k, a.batch, a.kv_heads, a.rows, false, &a.k)) ||
+      (rc = check_heads("v", v, a.batch, a.kv_heads, a.rows, false, &a.v)) ||
+      (rc = check_heads("out", out, a.batch, a.heads, a.rows, true, &a.out)))
+    return rc;
+  if (!lse) return fail(KLEIN_ERR_INVALID_ARG, "lse is NULL");
+  if (!element_aligned(lse, 1)) return fail(KLEIN_ERR_ALIGN, "lse is not aligned to its element");
+  a.lse = lse;
+  rc = launch_attention_train(a, static_cast<cudaStream_t>(stream));
+  if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  if (rc) return cuda_fail("attention launch");
+  return KLEIN_OK;
+}
+
+size_t klein_attention_backward_workspace_size(int batch, int heads, int rows, int n_txt) {
+  if (batch < 1 || heads < 1 || rows < 1 || n_txt < 0 || n_txt > rows) return 0;
+  return static_cast<size_t>(batch) * heads * attn_slots(rows, n_txt) * 256 * sizeof(float);
+}
+
+int klein_op_attention_backward(const klein_attention_shape* shape, const klein_heads* q, const klein_heads* k,
+                                const klein_heads* v, const klein_heads* out, const float* lse,
+                                const klein_heads* dout, const klein_heads* dq, const klein_heads* dk,
+                                const klein_heads* dv, void* ws, size_t ws_bytes, void* stream) {
+  AttnTrainArgs a{};
+  int rc = check_attention_shape(shape, &a);
+  if (rc || (rc = check_heads("q", q, a.batch, a.heads, a.rows, false, &a.q)) ||
+      (rc = check_heads("k", k, a.batch, a.kv_heads, a.rows, false, &a.k)) ||
+      (rc = check_heads("v", v, a.batch, a.kv_heads, a.rows, false, &a.v)) ||
+      (rc = check_heads("out", out, a.batch, a.heads, a.rows, false, &a.out)) ||
+      (rc = check_heads("dout", dout, a.batch, a.heads, a.rows, false, &a.dout)) ||
+      (rc = check_heads("dq", dq, a.batch, a.heads, a.rows, true, &a.dq)) ||
+      (rc = check_heads("dk", dk, a.batch, a.kv_heads, a.rows, true, &a.dk)) ||
+      (rc = check_heads("dv", dv, a.batch, a.kv_heads, a.rows, true, &a.dv)))
+    return rc;
+  if (!lse) return fail(KLEIN_ERR_INVALID_ARG, "lse is NULL");
+  if (!element_aligned(lse, 1)) return fail(KLEIN_ERR_ALIGN, "lse is not aligned to its element");
+  const size_t need = klein_attention_backward_workspace_size(a.batch, a.heads, a.rows, a.n_txt);
+  if (!ws || ws_bytes < need) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", need);
+  if (!aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  a.lse = const_cast<float*>(lse);  // only read by the backward kernels
+  a.stats = static_cast<float*>(ws);
+  rc = launch_attention_backward(a, static_cast<cudaStream_t>(stream));
+  if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  if (rc) return cuda_fail("attention backward launch");
+  return KLEIN_OK;
+}
+
 // ------------------------------------------------------------------ linear layer
 
 // Whether four columns at a time may be accessed: the address and the pitch
@@ -1147,8 +1272,6 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
 static int vec4_ok(const void* p, long long ld, int f32) {
   return (reinterpret_cast<uintptr_t>(p) & (f32 ? 15u : 7u)) == 0 && (ld % 4) == 0;
 }
-
-static bool element_aligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0; }
 
 static int check_linear_sizes(int m, int n, int k) {
   if (m < 1 || n < 1 || k < 1) return fail(KLEIN_ERR_SHAPE, "need m, n, k >= 1");
