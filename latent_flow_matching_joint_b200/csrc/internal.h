@@ -163,30 +163,35 @@ struct LinEpi {
   int act;
   int out_f32, res_f32;             // element types: fp32, else bf16
   int out_vec, res_vec, z_vec;      // four columns may be accessed at once (address and pitch allow it)
+  int vec;                          // ... of every matrix that there is
 };
 
 struct LinGemmArgs {
-  int m_tiles, n_tiles, k_blocks, splits;
-  int n_fastest;       // visit tiles N-fastest instead of M-fastest
-  float* partial;      // splits > 1: [splits][m][partial_ld] partial sums
-  long long partial_ld;
+  int m_tiles, n_tiles, k_blocks;
+  int k_wrap, a_low;   // from step k_wrap on, A's columns a_low further on against B's from the start
+  int waves, whole;    // the first `whole` tiles are dealt out whole, in `waves` rounds
+  int cut, shares;     // the last `cut` tiles are cut along k into `shares` equal shares, one per pair
+  int n_fastest;       // number the tiles N-fastest instead of M-fastest
+  float* partial;      // [2 * shares][part_rows][part_cols] sums of pieces of tiles
+  int part_rows, part_cols;
   LinEpi epi;
 };
 
 // One operand of C[m][n] = sum_k A(m, k) B(n, k): element (i, k) at data[i * ld + k],
 // or at data[k * ld + i] when mn_major. 16-byte aligned, ld a multiple of 8.
+// low > 0 (A only): the operand is the sum of two, the second `low` columns on.
 struct LinOperand {
   const void* data;
   long long ld;
   int mn_major;
+  int low;
 };
 
 struct LinPlan {
-  int pair, splits;
-  long long partial_ld;
-  size_t partial_bytes;  // workspace for partial sums, 0 without a split
+  int m_tiles, n_tiles, waves, whole, cut, shares, part_rows, part_cols;
+  size_t partial_bytes;  // workspace for pieces of tiles, 0 if none is cut
 };
-LinPlan plan_linear(long long m, long long n, long long k);
+LinPlan plan_linear(long long m, long long n, long long k_blocks);
 
 // The product and its epilogue (one or two launches). A row-contiguous only
 // together with B. Returns 0, -1 (launch) or -2 (tensor map).
@@ -209,6 +214,7 @@ struct LinDzArgs {
   float alpha;
   __nv_bfloat16* dz;    // [m][dz_ld], dz_ld a multiple of 8; or null
   long long dz_ld;
+  int low;              // > 0: the remainders of dz's rounding go `low` columns on
   float* col_part;      // [slabs][n] column sums of the slabs, or null
 };
 int lin_dz_slab(long long m, int n);

@@ -1275,8 +1275,9 @@ static int vec4_ok(const void* p, long long ld, int f32) {
 
 static int check_linear_sizes(int m, int n, int k) {
   if (m < 1 || n < 1 || k < 1) return fail(KLEIN_ERR_SHAPE, "need m, n, k >= 1");
-  // tile counts and grids are int
-  auto tiles = [](long long a, long long b) { return ((a + 127) / 128) * ((b + 127) / 128); };
+  // tile counts, grids and steps along k are int
+  if (m > (1 << 28) || n > (1 << 28) || k > (1 << 28)) return fail(KLEIN_ERR_SHAPE, "matrix too large");
+  auto tiles = [](long long a, long long b) { return ((a + 255) / 256) * ((b + 255) / 256); };
   if (tiles(m, n) > (1 << 26) || tiles(m, k) > (1 << 26) || tiles(n, k) > (1 << 26))
     return fail(KLEIN_ERR_SHAPE, "matrix too large");
   return KLEIN_OK;
@@ -1297,7 +1298,7 @@ static int check_matrix(const char* name, const void* p, long long ld, int cols,
 
 size_t klein_linear_workspace_size(int m, int n, int k) {
   if (m < 1 || n < 1 || k < 1 || m <= kLinMaxRows) return 0;
-  return plan_linear(m, n, k).partial_bytes;
+  return plan_linear(m, n, ((long long)k + 63) / 64).partial_bytes;
 }
 
 int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -1330,6 +1331,7 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
   e.z = static_cast<__nv_bfloat16*>(a->preact);
   e.z_ld = a->preact_ld;
   e.z_vec = vec4_ok(a->preact, a->preact_ld, 0);
+  e.vec = e.out_vec && (!e.res || e.res_vec) && (!e.z || e.z_vec);
   e.alpha = a->alpha;
   e.act = a->act;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1337,27 +1339,35 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
     rc = launch_linear_rows(static_cast<const __nv_bfloat16*>(a->x), a->x_ld, static_cast<const __nv_bfloat16*>(a->w),
                             a->w_ld, a->k, e, s);
   else
-    rc = launch_linear_gemm({a->x, a->x_ld, 0}, {a->w, a->w_ld, 0}, a->k, e, static_cast<float*>(ws), s);
+    rc = launch_linear_gemm({a->x, a->x_ld, 0, 0}, {a->w, a->w_ld, 0, 0}, a->k, e, static_cast<float*>(ws), s);
   if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   if (rc) return cuda_fail("linear launch");
   return KLEIN_OK;
 }
 
-// Workspace of klein_op_linear_backward: dz, the slabs' column sums, and the
-// partial sums of the larger of the two split products (they run one after
-// the other).
+// Workspace of klein_op_linear_backward: dz (with its remainders), the slabs'
+// column sums, and the pieces of tiles of the larger of the two products (they
+// run one after the other; with remainders or without).
 struct LinearGradWs {
   size_t dz, col_part, partial, bytes;
+  int dz_cols;  // n rounded up so that a product's steps through dz end with it
 };
 
 static LinearGradWs carve_linear_grad(int m, int n, int k) {
   LinearGradWs w{};
   const size_t slab = lin_dz_slab(m, n);
-  const size_t dx = plan_linear(m, k, n).partial_bytes, dw = plan_linear(n, k, m).partial_bytes;
+  size_t partial = 0;
+  for (int passes = 1; passes <= 2; ++passes) {
+    const size_t dx = plan_linear(m, k, ((long long)n + 63) / 64 * passes).partial_bytes;
+    const size_t dw = plan_linear(n, k, ((long long)m + 63) / 64 * passes).partial_bytes;
+    if (dx > partial) partial = dx;
+    if (dw > partial) partial = dw;
+  }
+  w.dz_cols = round_up(n, 64);
   w.dz = 0;
-  w.col_part = w.dz + align256((size_t)m * (((size_t)n + 7) / 8 * 8) * 2);
+  w.col_part = w.dz + align256((size_t)m * w.dz_cols * 2 * 2);
   w.partial = w.col_part + align256(((size_t)m + slab - 1) / slab * n * 4);
-  w.bytes = w.partial + align256(dx > dw ? dx : dw);
+  w.bytes = w.partial + align256(partial);
   return w;
 }
 
@@ -1392,7 +1402,10 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
   // from dz (alpha then goes into their epilogues) and TMA can read it.
   const bool direct = a->act == KLEIN_ACT_NONE && !a->dout_f32 && aligned16(a->dout) && (a->dout_ld % 8) == 0;
   const bool products = a->dx || a->dw;
-  LinOperand dz{a->dout, a->dout_ld, 0};
+  // An fp32 gradient is not to carry dz's rounding to bf16: it takes the
+  // remainders as well, in a second pass over the same product.
+  const bool fine = !direct && ((a->dx && a->dx_f32) || (a->dw && a->dw_f32));
+  LinOperand dz{a->dout, a->dout_ld, 0, 0};
   if ((products && !direct) || a->dbias) {
     LinDzArgs d{};
     d.m = a->m;
@@ -1409,8 +1422,9 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     d.alpha = a->alpha;
     if (products && !direct) {
       d.dz = reinterpret_cast<__nv_bfloat16*>(base + w.dz);
-      d.dz_ld = ((long long)a->n + 7) / 8 * 8;
-      dz = {d.dz, d.dz_ld, 0};
+      d.dz_ld = (long long)w.dz_cols * (fine ? 2 : 1);
+      d.low = fine ? w.dz_cols : 0;
+      dz = {d.dz, d.dz_ld, 0, 0};
     }
     d.col_part = a->dbias ? reinterpret_cast<float*>(base + w.col_part) : nullptr;
     if (launch_linear_dz(d, a->dbias, s)) return cuda_fail("linear gradient launch");
@@ -1425,8 +1439,9 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     e.out = a->dx;
     e.out_ld = a->dx_ld;
     e.out_f32 = a->dx_f32 != 0;
-    e.out_vec = vec4_ok(a->dx, a->dx_ld, e.out_f32);
-    rc = launch_linear_gemm(dz, {a->w, a->w_ld, 1}, a->n, e, partial, s);
+    e.vec = e.out_vec = vec4_ok(a->dx, a->dx_ld, e.out_f32);
+    dz.low = fine && e.out_f32 ? w.dz_cols : 0;
+    rc = launch_linear_gemm(dz, {a->w, a->w_ld, 1, 0}, a->n, e, partial, s);
     if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     if (rc) return cuda_fail("linear gradient launch");
   }
@@ -1436,9 +1451,10 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     e.out = a->dw;
     e.out_ld = a->dw_ld;
     e.out_f32 = a->dw_f32 != 0;
-    e.out_vec = vec4_ok(a->dw, a->dw_ld, e.out_f32);
+    e.vec = e.out_vec = vec4_ok(a->dw, a->dw_ld, e.out_f32);
     dz.mn_major = 1;
-    rc = launch_linear_gemm(dz, {a->x, a->x_ld, 1}, a->m, e, partial, s);
+    dz.low = fine && e.out_f32 ? w.dz_cols : 0;
+    rc = launch_linear_gemm(dz, {a->x, a->x_ld, 1, 0}, a->m, e, partial, s);
     if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     if (rc) return cuda_fail("linear gradient launch");
   }

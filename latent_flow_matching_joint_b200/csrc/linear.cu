@@ -9,20 +9,26 @@
 // 128-byte-swizzled tiles, and the MMA's operand descriptors and major bits
 // read either, so no transposed copy of anything is made.
 //
-// linear_gemm_kernel (320 threads): warp 0 TMA, warp 1 MMA issue, warps 2..9
-// epilogue (two per TMEM lane quarter, half of the tile's columns each). Two
-// shapes with the same 6 x 32 KB ring: CTA pairs with 256 x 256 tiles, and
-// single CTAs with 128 x 128 tiles for problems with too few large tiles,
-// with the sum over k split across CTAs when even those leave SMs idle
-// (partial sums in the workspace, added in split order by
-// linear_finish_kernel: no atomics, the same bits every run).
+// linear_gemm_kernel: persistent CTA pairs, 256 x 256 output tiles, 6 x 32 KB
+// ring, 384 threads: warp 0 TMA, warp 1 MMA issue, warps 4..11 epilogue (two
+// per TMEM lane quarter, half of the tile's columns each), two TMEM accumulators so
+// that a tile's epilogue overlaps the next one's main loop.
+//
+// Work is dealt out in whole tiles, one per pair and wave. The tiles of the last,
+// partial wave are cut along k into equal shares for all pairs when the plan
+// finds that faster (few tiles, long k): a share that is not a whole
+// tile leaves its sums in the workspace, and linear_finish_kernel adds a
+// tile's shares in the order of k and applies the epilogue. No atomics and no
+// waiting between pairs: the same bits every run.
 //
 // Sums: the tensor core truncates as it accumulates, which costs a relative
 // error of about 1.1e-9 per element of k (measured: 1.0e-5 at k = 9216, 2.3e-5
-// at 20480, against 1e-6 for fp32 FMAs). So the accumulator is moved out of
-// TMEM every 512 elements of k and added up in the epilogue warps' registers
-// with rounding to nearest, while the tensor core fills the other of two
-// accumulators; the epilogue warps are otherwise idle during the main loop.
+// at 20480, against 1e-6 for fp32 FMAs). That is far below a bf16 output's
+// rounding (2^-9), but not below an fp32 output's. So for fp32 outputs (FINE)
+// the accumulator is moved out of TMEM every 512 elements of k and added up in
+// the epilogue warps' registers with rounding to nearest, while the tensor
+// core fills the other accumulator; these warps take registers over from the
+// first four (3 x 168 = 72 + 2 x 216 per thread).
 #include "common.cuh"
 #include "internal.h"
 
@@ -36,9 +42,10 @@ constexpr int kLinStages = 6;
 constexpr int kLinRing = kLinStages * kLinStage;
 constexpr int kLinStaging = 8 * 4096;          // per epilogue warp: 32 rows x 32 fp32 columns
 constexpr int kLinSmem = kLinRing + kLinStaging + 256 + 1024;
-constexpr int kLinThreads = 320;
-constexpr int kLinChunk = 8;                   // k blocks (of 64) per TMEM accumulation
-constexpr int kLinPlanSms = 148;               // the B200's SM count: plans and workspace sizes do not depend on the device
+constexpr int kLinThreads = 384;
+constexpr int kLinChunk = 8;                   // FINE: k blocks (of 64) per TMEM accumulation
+constexpr int kLinSms = 148;                   // the B200's SM count: plans and workspace sizes do not depend on the device
+constexpr int kLinPairs = kLinSms / 2;
 
 // Shared-memory descriptor of an operand tile that is contiguous along its
 // row index (MN-major), written by TMA in boxes of 64 rows x 64 k with
@@ -141,6 +148,11 @@ __device__ __forceinline__ void lin_finish4(const LinEpi& e, long long row, int 
   }
 }
 
+// First step (64 of k) of share s, counted through the cut tiles one after the other.
+__device__ __forceinline__ int lin_share(const LinGemmArgs& g, int s) {
+  return static_cast<int>(static_cast<long long>(g.cut) * g.k_blocks * s / g.shares);
+}
+
 __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
   float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
   if (e.bias) {
@@ -154,13 +166,139 @@ __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
 
 }  // namespace
 
-// One work item = (output tile, share of k): item i is tile i % tiles, split i / tiles.
-template <bool AMN, bool BMN, bool PAIR>
+// A pair's share of the work: for w < waves the whole tile w * pairs + pair,
+// then up to two pieces of the cut tiles (a share is at most one tile long).
+struct LinPiece {
+  int mi, ni, kb0, kb1;
+  int slot;  // where its sums go in the workspace, or -1: a whole tile, finished here
+};
+
+__device__ __forceinline__ bool lin_piece(const LinGemmArgs& g, int pair, int i, LinPiece& p) {
+  int tile;
+  p.kb0 = 0;
+  p.kb1 = g.k_blocks;
+  p.slot = -1;
+  if (i < g.waves) {
+    tile = i * kLinPairs + pair;
+    if (tile >= g.whole) return false;
+  } else {
+    const int part = i - g.waves;
+    if (part > 1 || pair >= g.shares) return false;
+    const int u0 = lin_share(g, pair), u1 = lin_share(g, pair + 1);
+    const int t0 = u0 / g.k_blocks;
+    const int edge = (t0 + 1) * g.k_blocks;  // end of the share's first tile
+    if (part == 1 && u1 <= edge) return false;
+    tile = g.whole + t0 + part;
+    p.kb0 = part == 0 ? u0 - t0 * g.k_blocks : 0;
+    p.kb1 = part == 0 ? (u1 < edge ? u1 - t0 * g.k_blocks : g.k_blocks) : u1 - edge;
+    p.slot = 2 * pair + part;
+  }
+  p.mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
+  p.ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
+  return true;
+}
+
+// Epilogue of ROWS rows (rr = 4 r + sub, r < ROWS) x 4 columns per lane of a
+// warp's 32 x 32 piece, whose sums lie in shared memory.
+template <int ROWS>
+__device__ __forceinline__ void lin_finish_block(const LinEpi& e, const float* stg, int r0, long long row0, int col,
+                                                 int sub, int c4) {
+  float4 v[ROWS];
+  float4 res[ROWS];
+  const int rows_left = static_cast<int>(e.m - row0 < 32 ? e.m - row0 : 32);
+  const bool vec = e.vec && col + 4 <= e.n;
+  if (!vec) {  // odd widths, pitches and addresses: element by element
+    const float4 bias = lin_bias4(e, col);
+#pragma unroll 1
+    for (int r = 0; r < ROWS; ++r) {
+      const int rr = 4 * (r0 + r) + sub;
+      if (rr < rows_left && col < e.n)
+        lin_finish4(e, row0 + rr, col, *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2)), bias);
+    }
+    return;
+  }
+  if (e.res) {  // all of them in flight at once
+    if (e.res_f32) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int rr = 4 * (r0 + r) + sub;
+        if (rr < rows_left)
+          res[r] = *reinterpret_cast<const float4*>(static_cast<const float*>(e.res) + (row0 + rr) * e.res_ld + col);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int rr = 4 * (r0 + r) + sub;
+        if (rr < rows_left) {
+          const uint2 t =
+              *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.res) + (row0 + rr) * e.res_ld + col);
+          const float2 lo = unpack_bf16(t.x), hi = unpack_bf16(t.y);
+          res[r] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int rr = 4 * (r0 + r) + sub;
+    v[r] = *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2));
+  }
+  if (e.bias) {
+    const float4 bias = lin_bias4(e, col);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      v[r].x += bias.x;
+      v[r].y += bias.y;
+      v[r].z += bias.z;
+      v[r].w += bias.w;
+    }
+  }
+  if (e.z) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int rr = 4 * (r0 + r) + sub;
+      if (rr < rows_left)
+        *reinterpret_cast<uint2*>(e.z + (row0 + rr) * e.z_ld + col) =
+            make_uint2(pack_bf16(v[r].x, v[r].y), pack_bf16(v[r].z, v[r].w));
+    }
+  }
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      v[r].x = lin_act(v[r].x, e.act);
+      v[r].y = lin_act(v[r].y, e.act);
+      v[r].z = lin_act(v[r].z, e.act);
+      v[r].w = lin_act(v[r].w, e.act);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const float4 t = e.res ? res[r] : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[r] = make_float4(fmaf(e.alpha, v[r].x, t.x), fmaf(e.alpha, v[r].y, t.y), fmaf(e.alpha, v[r].z, t.z),
+                       fmaf(e.alpha, v[r].w, t.w));
+  }
+  if (e.out_f32) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int rr = 4 * (r0 + r) + sub;
+      if (rr < rows_left)
+        *reinterpret_cast<float4*>(static_cast<float*>(e.out) + (row0 + rr) * e.out_ld + col) = v[r];
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int rr = 4 * (r0 + r) + sub;
+      if (rr < rows_left)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.out) + (row0 + rr) * e.out_ld + col) =
+            make_uint2(pack_bf16(v[r].x, v[r].y), pack_bf16(v[r].z, v[r].w));
+    }
+  }
+}
+
+template <bool AMN, bool BMN, bool FINE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const LinGemmArgs g) {
-  constexpr int kTileM = PAIR ? 256 : 128, kTileN = kTileM;
-  constexpr int kCols = kTileN / 2;  // accumulator columns per epilogue thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLinRing + kLinStaging);
@@ -172,7 +310,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
 
   if (warp == 0 && lane == 0) {
@@ -182,7 +320,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], PAIR ? 512 : 256);
+      mbar_init(&acc_empty[a], 16);  // one arrival per epilogue warp of the pair
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -190,71 +328,62 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tma_prefetch_desc(&map_b);
   }
   if (warp == 1) {
-    if (PAIR) {
-      tmem_alloc_pair(tmem_slot, 2 * kTileN);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, 2 * kTileN);
-      tmem_relinquish();
-    }
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  if (PAIR) cluster_sync(); else __syncthreads();
+  cluster_sync();  // barrier initialisation and the TMEM allocation are visible pair-wide
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_trigger();
   pdl_wait();  // operands and outputs are touched only after the previous kernel completes
 
-  const int tiles = g.m_tiles * g.n_tiles;
-  const int items = tiles * g.splits;
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-  const int step = PAIR ? gridDim.x >> 1 : gridDim.x;
-  constexpr uint32_t idesc =
-      idesc_bf16_f32(kTileM, kTileN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
-  auto k_begin = [&](int split) { return static_cast<int>(static_cast<long long>(g.k_blocks) * split / g.splits); };
+  const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+  LinPiece p;
 
+  if (warp < 4) {
+    if (FINE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       StageLog log;
       bool ok = true;
-      for (int item = first; ok && item < items; item += step) {
-        const int tile = item % tiles, split = item / tiles;
-        const int mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
-        const int ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
-        const int row = mi * kTileM + 128 * rank, col = ni * kTileN + 128 * rank;
-        const int kb1 = k_begin(split + 1);
-        for (int kb = k_begin(split); kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, 0x301)) { ok = false; break; }
-          if (leader) {
-            mbar_arrive_expect_tx(&full[stage], PAIR ? 2 * kLinStage : kLinStage);
-            log.armed(stage, phase);
+      for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+        for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
+          const int row = p.mi * 256 + 128 * rank, col = p.ni * 256 + 128 * rank;
+          for (int kb = p.kb0; kb < p.kb1; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, 0x301)) { ok = false; break; }
+            if (leader) {
+              mbar_arrive_expect_tx(&full[stage], 2 * kLinStage);
+              log.armed(stage, phase);
+            }
+            uint8_t* sa = smem + stage * kLinStage;
+            uint8_t* sb = sa + kLinTile;
+            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+            // the second pass over k reads A's low halves against the same B
+            const int kb_b = kb >= g.k_wrap ? kb - g.k_wrap : kb;
+            if (AMN) {
+              const int r = kb >= g.k_wrap ? row + g.a_low : row;
+              tma_load_2d_pair(sa, &map_a, bar, r, kb_b * 64);
+              tma_load_2d_pair(sa + kLinTile / 2, &map_a, bar, r + 64, kb_b * 64);
+            } else {
+              tma_load_2d_pair(sa, &map_a, bar, kb >= g.k_wrap ? kb_b * 64 + g.a_low : kb * 64, row);
+            }
+            if (BMN) {
+              tma_load_2d_pair(sb, &map_b, bar, col, kb_b * 64);
+              tma_load_2d_pair(sb + kLinTile / 2, &map_b, bar, col + 64, kb_b * 64);
+            } else {
+              tma_load_2d_pair(sb, &map_b, bar, kb_b * 64, col);
+            }
+            if (++stage == kLinStages) { stage = 0; phase ^= 1; }
           }
-          uint8_t* sa = smem + stage * kLinStage;
-          uint8_t* sb = sa + kLinTile;
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1) {
-            if (PAIR) tma_load_2d_pair(dst, map, mapa_shared(smem_u32(&full[stage]), 0), c0, c1);
-            else tma_load_2d(dst, map, &full[stage], c0, c1);
-          };
-          if (AMN) {
-            load(sa, &map_a, row, kb * 64);
-            load(sa + kLinTile / 2, &map_a, row + 64, kb * 64);
-          } else {
-            load(sa, &map_a, kb * 64, row);
-          }
-          if (BMN) {
-            load(sb, &map_b, col, kb * 64);
-            load(sb + kLinTile / 2, &map_b, col + 64, kb * 64);
-          } else {
-            load(sb, &map_b, kb * 64, col);
-          }
-          if (++stage == kLinStages) { stage = 0; phase ^= 1; }
         }
       }
-      // No TMA write of this CTA (or pair: the leader's barriers count both
-      // CTAs' bytes, and the cluster barrier below keeps the other CTA alive)
-      // may land after it exits.
+      // No TMA write of the pair may land after it exits: the leader's
+      // barriers count both CTAs' bytes, and the cluster barrier below keeps
+      // the other CTA alive.
       if (leader) log.drain(full, kLinStages, 0x305);
     }
   } else if (warp == 1) {
@@ -263,109 +392,122 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t phase = 0;
       int chunk = 0;
       bool ok = true;
-      for (int item = first; ok && item < items; item += step) {
-        const int split = item / tiles;
-        const int kb0 = k_begin(split), kb1 = k_begin(split + 1);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const int in_chunk = (kb - kb0) % kLinChunk;
-          const int acc = chunk & 1;
-          if (in_chunk == 0) {
+      for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+        for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
+          for (int kb = p.kb0; ok && kb < p.kb1; ++chunk) {
+            const int acc = chunk & 1;
             if (!mbar_wait(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, 0x302)) { ok = false; break; }
             tc_fence_after();
-          }
-          if (!mbar_wait(&full[stage], phase, 0x303)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t d = tmem_base + acc * kTileN;
-          const uint32_t a0 = smem_u32(smem + stage * kLinStage);
-          const uint32_t b0 = a0 + kLinTile;
+            const uint32_t d = tmem_base + acc * 256;
+            const int first = kb;
+            const int end = FINE && kb + kLinChunk < p.kb1 ? kb + kLinChunk : p.kb1;
+            for (; kb < end; ++kb) {
+              if (!mbar_wait(&full[stage], phase, 0x303)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t a0 = smem_u32(smem + stage * kLinStage);
+              const uint32_t b0 = a0 + kLinTile;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = AMN ? sw128_desc_mn(a0 + 2048 * k, kLinTile / 2) : sw128_desc(a0 + 32 * k);
-            const uint64_t db = BMN ? sw128_desc_mn(b0 + 2048 * k, kLinTile / 2) : sw128_desc(b0 + 32 * k);
-            if (PAIR) umma_bf16_pair(d, da, db, idesc, (in_chunk | k) != 0);
-            else umma_bf16(d, da, db, idesc, (in_chunk | k) != 0);
-          }
-          if (PAIR) umma_commit_pair(&empty[stage], 0x3); else umma_commit(&empty[stage]);
-          if (++stage == kLinStages) { stage = 0; phase ^= 1; }
-          if (in_chunk == kLinChunk - 1 || kb == kb1 - 1) {
-            if (PAIR) umma_commit_pair(&acc_full[acc], 0x3); else umma_commit(&acc_full[acc]);
-            ++chunk;
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t da = AMN ? sw128_desc_mn(a0 + 2048 * k, kLinTile / 2) : sw128_desc(a0 + 32 * k);
+                const uint64_t db = BMN ? sw128_desc_mn(b0 + 2048 * k, kLinTile / 2) : sw128_desc(b0 + 32 * k);
+                umma_bf16_pair(d, da, db, idesc, kb != first || k != 0);
+              }
+              umma_commit_pair(&empty[stage], 0x3);
+              if (++stage == kLinStages) { stage = 0; phase ^= 1; }
+            }
+            if (ok) umma_commit_pair(&acc_full[acc], 0x3);
           }
         }
       }
       // every MMA issued here has completed before TMEM is freed
-      if (PAIR) umma_commit_pair(drain, 0x1); else umma_commit(drain);
+      umma_commit_pair(drain, 0x1);
       mbar_wait(drain, 0, 0x306);
     }
+    }
   } else {
+    if (FINE) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;
-    const int part = (warp - 2) >> 2;  // which half of the tile's columns
-    float* stg = reinterpret_cast<float*>(smem + kLinRing + (warp - 2) * 4096);
-    const int sub = lane >> 3, c4 = lane & 7;  // after the transposition: row 4 i + sub, columns 4 c4..4 c4 + 3
+    const int part = (warp - 4) >> 2;  // which half of the tile's columns
+    float* stg = reinterpret_cast<float*>(smem + kLinRing + (warp - 4) * 4096);
+    const int sub = lane >> 3, c4 = lane & 7;  // after the transposition: rows 4 r + sub, columns 4 c4..4 c4 + 3
     int chunk = 0;
     bool ok = true;
-    for (int item = first; ok && item < items; item += step) {
-      const int tile = item % tiles, split = item / tiles;
-      const int mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
-      const int ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
-      const int chunks = (k_begin(split + 1) - k_begin(split) + kLinChunk - 1) / kLinChunk;
-      float acc[kCols];
-      for (int c = 0; c < chunks; ++c, ++chunk) {
-        const int buf = chunk & 1;
-        if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t taddr =
-            tmem_base + buf * kTileN + part * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
-        if (c == 0) {
+    auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+    };
+    // Each thread holds one row; through shared memory (16-byte chunks,
+    // XOR-swizzled by row) a warp's 32 x 32 piece turns into row segments,
+    // so that residual reads and output writes fill their sectors.
+    auto finish = [&](const float* v, int row0, int col0) {
+      __syncwarp();
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i) tmem_ld32(taddr + 32 * i, acc + 32 * i);
-        } else {
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      __syncwarp();
+      if (p.slot >= 0) {
+        float* dst = g.partial + (static_cast<long long>(p.slot) * g.part_rows + (row0 - p.mi * 256)) * g.part_cols +
+                     (col0 - p.ni * 256) + 4 * c4;
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i) {
-            float v[32];
-            tmem_ld32(taddr + 32 * i, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[32 * i + j] += v[j];
-          }
+        for (int r = 0; r < 8; ++r) {
+          const int rr = 4 * r + sub;
+          if (row0 + rr < g.epi.m)
+            *reinterpret_cast<float4*>(dst + rr * g.part_cols) =
+                *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2));
         }
-        tc_fence_before();
-        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
-        else mbar_arrive(&acc_empty[buf]);
+      } else if (FINE) {
+        lin_finish_block<4>(g.epi, stg, 0, row0, col0 + 4 * c4, sub, c4);
+        lin_finish_block<4>(g.epi, stg, 4, row0, col0 + 4 * c4, sub, c4);
+      } else {
+        lin_finish_block<8>(g.epi, stg, 0, row0, col0 + 4 * c4, sub, c4);
       }
-      if (!ok) break;
-      // Each thread holds one row; through shared memory (16-byte chunks,
-      // XOR-swizzled by row) a warp's 32 x 32 piece turns into whole row
-      // segments, so that residual reads and output writes fill their sectors.
-      const int row0 = mi * kTileM + 128 * rank + quarter * 32;
-      const int col0 = ni * kTileN + part * kCols;
+    };
+    for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+      for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
+        const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
+        const int col0 = p.ni * 256 + part * 128;
+        if (FINE) {
+          const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
+          float acc[128];
+          for (int c = 0; c < chunks; ++c, ++chunk) {
+            const int buf = chunk & 1;
+            if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t taddr =
+                tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-      for (int i = 0; i < kCols / 32; ++i) {
-        if (row0 >= g.epi.m || col0 + 32 * i >= g.epi.n) break;
-        __syncwarp();
+            for (int j = 0; j < 4; ++j) {
+              if (c == 0) {
+                tmem_ld32(taddr + 32 * j, acc + 32 * j);
+              } else {
+                float v[32];
+                tmem_ld32(taddr + 32 * j, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
-              make_float4(acc[32 * i + 4 * j], acc[32 * i + 4 * j + 1], acc[32 * i + 4 * j + 2], acc[32 * i + 4 * j + 3]);
-        __syncwarp();
-        const int col = col0 + 32 * i + 4 * c4;
-        if (g.splits > 1) {
-          float* p = g.partial + (static_cast<long long>(split) * g.epi.m + row0) * g.partial_ld + col;
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int rr = 4 * r + sub;
-            if (row0 + rr < g.epi.m)
-              *reinterpret_cast<float4*>(p + rr * g.partial_ld) =
-                  *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2));
+                for (int q = 0; q < 32; ++q) acc[32 * j + q] += v[q];
+              }
+            }
+            release(buf);
           }
-        } else if (col < g.epi.n) {
-          const float4 bias = lin_bias4(g.epi, col);
-#pragma unroll 4
-          for (int r = 0; r < 8; ++r) {
-            const int rr = 4 * r + sub;
-            if (row0 + rr < g.epi.m)
-              lin_finish4(g.epi, row0 + rr, col, *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2)),
-                          bias);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row0 < g.epi.m && col0 + 32 * j < g.epi.n) finish(acc + 32 * j, row0, col0 + 32 * j);
+        } else {
+          const int buf = chunk & 1;
+          if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
+          ++chunk;
+          tc_fence_after();
+          const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            if (row0 >= g.epi.m || col0 + 32 * j >= g.epi.n) break;
+            float v[32];
+            tmem_ld32(taddr + 32 * j, v);
+            finish(v, row0, col0 + 32 * j);
           }
+          release(buf);
         }
       }
     }
@@ -373,32 +515,45 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   __syncwarp();
   tc_fence_before();
-  if (PAIR) cluster_sync(); else __syncthreads();  // every MMA and epilogue is done
+  cluster_sync();  // every MMA and every epilogue of both CTAs is done
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    if (PAIR) tmem_dealloc_pair(tmem_base, 2 * kTileN); else tmem_dealloc(tmem_base, 2 * kTileN);
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-// Adds the splits' partial sums in split order and applies the epilogue.
-__global__ void __launch_bounds__(256) linear_finish_kernel(const float* partial, long long partial_ld, int splits,
-                                                            const LinEpi e) {
+// The cut tiles: adds the shares' sums in the order of k and applies the
+// epilogue. One block takes 16 rows of one tile.
+__global__ void __launch_bounds__(256) linear_finish_kernel(const LinGemmArgs g) {
   pdl_trigger();
   pdl_wait();
-  const int groups = (e.n + 3) / 4;
-  const long long total = static_cast<long long>(e.m) * groups;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long row = i / groups;
-    const int col = static_cast<int>(i - row * groups) * 4;
-    const float* p = partial + row * partial_ld + col;
-    float4 s = *reinterpret_cast<const float4*>(p);
-    for (int k = 1; k < splits; ++k) {
-      const float4 t = *reinterpret_cast<const float4*>(p + k * (e.m * partial_ld));
-      s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+  const int t = blockIdx.x;  // among the cut tiles
+  const int tile = g.whole + t;
+  const int mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
+  const int ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
+  const int col = (threadIdx.x & 63) * 4;
+  if (ni * 256 + col >= g.epi.n) return;
+  const int u0 = t * g.k_blocks, u1 = u0 + g.k_blocks;
+  // first and last share with part of this tile
+  int s0 = static_cast<int>(static_cast<long long>(u0) * g.shares / (static_cast<long long>(g.cut) * g.k_blocks));
+  while (s0 > 0 && lin_share(g, s0) > u0) --s0;
+  while (lin_share(g, s0 + 1) <= u0) ++s0;
+  const float4 bias = lin_bias4(g.epi, ni * 256 + col);
+  for (int r = blockIdx.y * 16 + (threadIdx.x >> 6); r < blockIdx.y * 16 + 16; r += 4) {
+    const long long row = static_cast<long long>(mi) * 256 + r;
+    if (row >= g.epi.m) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = s0; s < g.shares && lin_share(g, s) < u1; ++s) {
+      const int slot = 2 * s + (lin_share(g, s) < u0 ? 1 : 0);  // the share began in the tile before
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(
+          g.partial + (static_cast<long long>(slot) * g.part_rows + r) * g.part_cols + col));
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
     }
-    lin_finish4(e, row, col, s, lin_bias4(e, col));
+    lin_finish4(g.epi, row, ni * 256 + col, v, bias);
   }
 }
 
@@ -485,7 +640,8 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const __nv_bfloat16* x
 }
 
 // dz = alpha * dy * act'(z) in bf16 (the operand type of the two products
-// after it) and, for dbias, the sum of each block's rows per column, from the
+// after it), with `low` also the bf16 remainder (the two together keep 16 bits
+// of mantissa, for products whose output is fp32), and, for dbias, the sum of each block's rows per column, from the
 // fp32 dz before that rounding. A block takes 256 columns (8 per lane) and a
 // slab of rows, its 8 warps every eighth row.
 __global__ void __launch_bounds__(256) linear_dz_kernel(const LinDzArgs a) {
@@ -499,7 +655,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinDzArgs a) {
   const int count = a.n - col < 8 ? (a.n - col < 0 ? 0 : a.n - col) : 8;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (long long r = r0 + warp; r < r1; r += 8) {
-    if (count <= 0) break;
+    if (count <= 0 && col >= a.low) break;
     float d[8];
     const long long di = r * a.dout_ld + col;
     if (count == 8 && a.dout_vec) {
@@ -538,9 +694,17 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinDzArgs a) {
       d[i] *= a.alpha;
       s[i] += d[i];
     }
-    if (a.dz)  // pitch a multiple of 8 columns: the padding columns get zeros
-      *reinterpret_cast<uint4*>(a.dz + r * a.dz_ld + col) =
+    if (a.dz) {  // columns of the padding get zeros, up to `low` with remainders (a product's steps run through them)
+      const uint4 hi =
           make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+      *reinterpret_cast<uint4*>(a.dz + r * a.dz_ld + col) = hi;
+      if (a.low) {  // what the rounding left, rounded in turn
+        const float2 h0 = unpack_bf16(hi.x), h1 = unpack_bf16(hi.y), h2 = unpack_bf16(hi.z), h3 = unpack_bf16(hi.w);
+        *reinterpret_cast<uint4*>(a.dz + r * a.dz_ld + a.low + col) =
+            make_uint4(pack_bf16(d[0] - h0.x, d[1] - h0.y), pack_bf16(d[2] - h1.x, d[3] - h1.y),
+                       pack_bf16(d[4] - h2.x, d[5] - h2.y), pack_bf16(d[6] - h3.x, d[7] - h3.y));
+      }
+    }
   }
   if (a.col_part) {
 #pragma unroll
@@ -570,104 +734,109 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, in
 
 // ------------------------------------------------------------------ host
 
-// Tile shape and split count of one product from its sizes alone. The cost
-// model counts tensor-core clocks of the busiest SM: a 64-deep step takes
-// about 512 clocks for a pair's 256 x 256 tile and 300 for a single CTA's
-// 128 x 128 (whose operand reads fill the shared-memory port), a tile's
-// unoverlapped start and epilogue about 3000, and a split sum costs a second
-// launch plus writing and reading the partial sums.
-LinPlan plan_linear(long long m, long long n, long long k) {
-  LinPlan best{};
-  double best_cost = 0;
-  const long long kb = (k + 63) / 64;
-  for (int pair = 0; pair < 2; ++pair) {
-    const long long t = pair ? 256 : 128;
-    const long long tiles = ((m + t - 1) / t) * ((n + t - 1) / t);
-    const long long slots = pair ? kLinPlanSms / 2 : kLinPlanSms;
-    for (int s = 1; s <= (pair ? 4 : 16); ++s) {
-      if (s > kb || (s > 1 && kb / s < 4)) break;
-      const double waves = static_cast<double>((tiles * s + slots - 1) / slots);
-      double cost = waves * (static_cast<double>((kb + s - 1) / s) * (pair ? 512 : 300) + 1000) + 2000;
-      if (s > 1) cost += 5000 + 2.0 * s * m * ((n + 127) / 128 * 128) * 4 / 2500.0;
-      if (best.splits == 0 || cost < best_cost) {
-        best_cost = cost;
-        best.pair = pair;
-        best.splits = s;
+// How one product's tiles are dealt out, from its sizes alone (k already
+// counted twice where A has low halves). Costs in tensor-core clocks: a
+// 64-deep step of a 256 x 256 tile takes about 560; cutting the last wave's
+// tiles adds a second launch and the trip of every share's sums through L2.
+LinPlan plan_linear(long long m, long long n, long long k_blocks) {
+  LinPlan p{};
+  p.m_tiles = static_cast<int>((m + 255) / 256);
+  p.n_tiles = static_cast<int>((n + 255) / 256);
+  const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
+  p.part_rows = static_cast<int>(m < 256 ? m : 256);
+  p.part_cols = static_cast<int>(n < 256 ? (n + 31) / 32 * 32 : 256);
+  p.whole = static_cast<int>(tiles);
+  p.waves = static_cast<int>((tiles + kLinPairs - 1) / kLinPairs);
+  const int rest = static_cast<int>(tiles % kLinPairs);
+  if (rest > 0) {
+    const long long units = rest * k_blocks;
+    long long shares = units / 4 < kLinPairs ? units / 4 : kLinPairs;  // at least 4 steps each
+    if (shares > rest) {
+      const double tile_bytes = 4.0 * p.part_rows * p.part_cols;
+      const double cut = static_cast<double>((units + shares - 1) / shares) * 560 + 6000 +
+                         2 * (shares + rest) * tile_bytes / 4000;
+      if (cut < static_cast<double>(k_blocks) * 560) {
+        p.cut = rest;
+        p.shares = static_cast<int>(shares);
+        p.whole = static_cast<int>(tiles) - rest;
+        p.waves = p.whole / kLinPairs;
+        p.partial_bytes = 2 * static_cast<size_t>(shares) * p.part_rows * p.part_cols * 4;
       }
     }
   }
-  best.partial_ld = (n + 127) / 128 * 128;
-  best.partial_bytes = best.splits > 1 ? static_cast<size_t>(best.splits) * m * best.partial_ld * 4 : 0;
-  return best;
+  return p;
 }
 
-template <bool AMN, bool BMN, bool PAIR>
+template <bool AMN, bool BMN, bool FINE>
 static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const LinGemmArgs& g, cudaStream_t s) {
-  static int slots_dev[kMaxDevices] = {};
+  static int pairs_dev[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return -1;
-  int& slots = slots_dev[dev];
-  auto kernel = linear_gemm_kernel<AMN, BMN, PAIR>;
-  if (slots == 0) {
+  int& pairs = pairs_dev[dev];
+  auto kernel = linear_gemm_kernel<AMN, BMN, FINE>;
+  if (pairs == 0) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem) != cudaSuccess) return -1;
-    int n = num_sms();
-    if (PAIR) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(2 * (n / 2));
-      cfg.blockDim = dim3(kLinThreads);
-      cfg.dynamicSmemBytes = kLinSmem;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return -1;
-    }
-    slots = n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * kLinPairs);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kLinSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return -1;
+    pairs = n < kLinPairs ? n : kLinPairs;
   }
-  const long long items = static_cast<long long>(g.m_tiles) * g.n_tiles * g.splits;
-  const int groups = static_cast<int>(items < slots ? items : slots);
-  const cudaError_t e = launch_kernel(kernel, dim3(PAIR ? 2 * groups : groups), dim3(kLinThreads), kLinSmem, s,
-                                      PAIR ? 2 : 1, ma, mb, g);
+  const int busy = g.waves > 0 ? (g.whole < kLinPairs ? g.whole : kLinPairs) : g.shares;
+  const int grid = busy < pairs ? busy : pairs;
+  const cudaError_t e = launch_kernel(kernel, dim3(2 * grid), dim3(kLinThreads), kLinSmem, s, 2, ma, mb, g);
   note_launch();
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
 
 int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const LinEpi& epi, float* partial,
                        cudaStream_t s) {
-  const LinPlan plan = plan_linear(epi.m, epi.n, k);
-  const int tile = plan.pair ? 256 : 128;
+  const int kb = (k + 63) / 64;
+  const int passes = a.low ? 2 : 1;
+  const LinPlan plan = plan_linear(epi.m, epi.n, static_cast<long long>(kb) * passes);
   CUtensorMap ma, mb;
-  auto encode = [&](CUtensorMap* map, const LinOperand& o, int rows) {
-    // box: 64 k x 128 rows of a k-contiguous operand, 64 rows x 64 k of a row-contiguous one
-    return o.mn_major ? make_map_2d(map, o.data, rows, k, static_cast<uint64_t>(o.ld) * 2, 64, 64)
-                      : make_map_2d(map, o.data, k, rows, static_cast<uint64_t>(o.ld) * 2, 64, 128);
-  };
-  if (encode(&ma, a, epi.m) || encode(&mb, b, epi.n)) return -2;
+  // box: 64 k x 128 rows of a k-contiguous operand, 64 rows x 64 k of a
+  // row-contiguous one; A's low halves follow its high ones a.low columns on
+  const uint64_t a_inner = static_cast<uint64_t>(a.mn_major ? epi.m : k) + a.low;
+  if (make_map_2d(&ma, a.data, a_inner, a.mn_major ? k : epi.m, static_cast<uint64_t>(a.ld) * 2, 64,
+                  a.mn_major ? 64 : 128) ||
+      make_map_2d(&mb, b.data, b.mn_major ? epi.n : k, b.mn_major ? k : epi.n, static_cast<uint64_t>(b.ld) * 2, 64,
+                  b.mn_major ? 64 : 128))
+    return -2;
   LinGemmArgs g{};
-  g.m_tiles = (epi.m + tile - 1) / tile;
-  g.n_tiles = (epi.n + tile - 1) / tile;
-  g.k_blocks = (k + 63) / 64;
-  g.splits = plan.splits;
+  g.m_tiles = plan.m_tiles;
+  g.n_tiles = plan.n_tiles;
+  g.k_blocks = kb * passes;
+  g.k_wrap = kb;
+  g.a_low = a.low;
+  g.waves = plan.waves;
+  g.whole = plan.whole;
+  g.cut = plan.cut;
+  g.shares = plan.shares;
   g.n_fastest = epi.n <= epi.m;  // the smaller operand stays in L2, the larger streams through once
   g.partial = partial;
-  g.partial_ld = plan.partial_ld;
+  g.part_rows = plan.part_rows;
+  g.part_cols = plan.part_cols;
   g.epi = epi;
   int rc;
   if (!a.mn_major && !b.mn_major)
-    rc = plan.pair ? launch_lin_one<false, false, true>(ma, mb, g, s) : launch_lin_one<false, false, false>(ma, mb, g, s);
+    rc = epi.out_f32 ? launch_lin_one<false, false, true>(ma, mb, g, s) : launch_lin_one<false, false, false>(ma, mb, g, s);
   else if (!a.mn_major)
-    rc = plan.pair ? launch_lin_one<false, true, true>(ma, mb, g, s) : launch_lin_one<false, true, false>(ma, mb, g, s);
+    rc = epi.out_f32 ? launch_lin_one<false, true, true>(ma, mb, g, s) : launch_lin_one<false, true, false>(ma, mb, g, s);
   else
-    rc = plan.pair ? launch_lin_one<true, true, true>(ma, mb, g, s) : launch_lin_one<true, true, false>(ma, mb, g, s);
-  if (rc || plan.splits == 1) return rc;
-  const long long quads = static_cast<long long>(epi.m) * ((epi.n + 3) / 4);
-  const long long blocks = (quads + 255) / 256;
-  const int grid = static_cast<int>(blocks < 8 * kLinPlanSms ? blocks : 8 * kLinPlanSms);
-  const cudaError_t e = launch_kernel(linear_finish_kernel, dim3(grid), dim3(256), 0, s, 1,
-                                      static_cast<const float*>(partial), g.partial_ld, plan.splits, epi);
+    rc = epi.out_f32 ? launch_lin_one<true, true, true>(ma, mb, g, s) : launch_lin_one<true, true, false>(ma, mb, g, s);
+  if (rc || !plan.cut) return rc;
+  const cudaError_t e =
+      launch_kernel(linear_finish_kernel, dim3(plan.cut, (plan.part_rows + 15) / 16), dim3(256), 0, s, 1, g);
   note_launch();
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
@@ -675,7 +844,7 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
 template <int MV>
 static cudaError_t launch_rows_mv(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                                   const LinEpi& e, cudaStream_t s) {
-  if (e.n < 8 * kLinPlanSms && k >= 2048)  // one warp per column would leave most SMs with a few long serial rows
+  if (e.n < 8 * kLinSms && k >= 2048)  // one warp per column would leave most SMs with a few long serial rows
     return launch_kernel(linear_rows_kernel<MV, 8>, dim3(e.n), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
   return launch_kernel(linear_rows_kernel<MV, 1>, dim3((e.n + 7) / 8), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
 }
@@ -694,7 +863,7 @@ int launch_linear_rows(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat
 // multiple of the 8 rows that a block's warps take at a time.
 int lin_dz_slab(long long m, int n) {
   const long long col_blocks = (n + 255) / 256;
-  long long slabs = (4 * kLinPlanSms + col_blocks - 1) / col_blocks;
+  long long slabs = (4 * kLinSms + col_blocks - 1) / col_blocks;
   const long long most = (m + 31) / 32;
   if (slabs > most) slabs = most;
   if (slabs < 1) slabs = 1;
