@@ -170,9 +170,9 @@ struct LinGemmArgs {
   int m_tiles, n_tiles, k_blocks;
   int k_wrap, a_low;   // from step k_wrap on, A's columns a_low further on against B's from the start
   int waves, whole;    // the first `whole` tiles are dealt out whole, in `waves` rounds
-  int cut, shares;     // the last `cut` tiles are cut along k into `shares` equal shares, one per pair
+  int cut, parts;      // the last `cut` tiles are cut along k into `parts` equal parts each
   int n_fastest;       // number the tiles N-fastest instead of M-fastest
-  float* partial;      // [2 * shares][part_rows][part_cols] sums of pieces of tiles
+  float* partial;      // [parts][cut][part_rows][part_cols] the parts' sums
   int part_rows, part_cols;
   LinEpi epi;
 };
@@ -188,8 +188,8 @@ struct LinOperand {
 };
 
 struct LinPlan {
-  int m_tiles, n_tiles, waves, whole, cut, shares, part_rows, part_cols;
-  size_t partial_bytes;  // workspace for pieces of tiles, 0 if none is cut
+  int m_tiles, n_tiles, waves, whole, cut, parts, part_rows, part_cols;
+  size_t partial_bytes;  // workspace for the parts' sums, 0 if no tile is cut
 };
 LinPlan plan_linear(long long m, long long n, long long k_blocks);
 

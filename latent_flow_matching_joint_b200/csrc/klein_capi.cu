@@ -1346,8 +1346,8 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
 }
 
 // Workspace of klein_op_linear_backward: dz (with its remainders), the slabs'
-// column sums, and the pieces of tiles of the larger of the two products (they
-// run one after the other; with remainders or without).
+// column sums, and the parts' sums of the larger of the two products (they run
+// one after the other; with remainders or without).
 struct LinearGradWs {
   size_t dz, col_part, partial, bytes;
   int dz_cols;  // n rounded up so that a product's steps through dz end with it

@@ -15,11 +15,14 @@
 // that a tile's epilogue overlaps the next one's main loop.
 //
 // Work is dealt out in whole tiles, one per pair and wave. The tiles of the last,
-// partial wave are cut along k into equal shares for all pairs when the plan
-// finds that faster (few tiles, long k): a share that is not a whole
-// tile leaves its sums in the workspace, and linear_finish_kernel adds a
-// tile's shares in the order of k and applies the epilogue. No atomics and no
-// waiting between pairs: the same bits every run.
+// partial wave are cut into equal parts along k when the plan finds that
+// faster (few tiles, long k). Parts are dealt out part by part, so that the
+// pairs at work read the same stretch of k of the operands; their sums go to
+// the workspace, and linear_finish_kernel adds a tile's parts in the order of
+// k and applies the epilogue. No atomics and no waiting between pairs: the
+// same bits every run. (Shares of equal length that run across tiles balance
+// a little better but spread over k: 1024 x 3072 x 20480, whose operands do
+// not fit L2, took 124 us that way.)
 //
 // Sums: the tensor core truncates as it accumulates, which costs a relative
 // error of about 1.1e-9 per element of k (measured: 1.0e-5 at k = 9216, 2.3e-5
@@ -148,11 +151,6 @@ __device__ __forceinline__ void lin_finish4(const LinEpi& e, long long row, int 
   }
 }
 
-// First step (64 of k) of share s, counted through the cut tiles one after the other.
-__device__ __forceinline__ int lin_share(const LinGemmArgs& g, int s) {
-  return static_cast<int>(static_cast<long long>(g.cut) * g.k_blocks * s / g.shares);
-}
-
 __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
   float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
   if (e.bias) {
@@ -167,34 +165,34 @@ __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
 }  // namespace
 
 // A pair's share of the work: for w < waves the whole tile w * pairs + pair,
-// then up to two pieces of the cut tiles (a share is at most one tile long).
+// then every kLinPairs-th of the cut tiles' parts.
 struct LinPiece {
   int mi, ni, kb0, kb1;
   int slot;  // where its sums go in the workspace, or -1: a whole tile, finished here
 };
 
+__device__ __forceinline__ void lin_tile(const LinGemmArgs& g, int tile, int& mi, int& ni) {
+  mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
+  ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
+}
+
 __device__ __forceinline__ bool lin_piece(const LinGemmArgs& g, int pair, int i, LinPiece& p) {
-  int tile;
-  p.kb0 = 0;
-  p.kb1 = g.k_blocks;
-  p.slot = -1;
   if (i < g.waves) {
-    tile = i * kLinPairs + pair;
+    const int tile = i * kLinPairs + pair;
     if (tile >= g.whole) return false;
-  } else {
-    const int part = i - g.waves;
-    if (part > 1 || pair >= g.shares) return false;
-    const int u0 = lin_share(g, pair), u1 = lin_share(g, pair + 1);
-    const int t0 = u0 / g.k_blocks;
-    const int edge = (t0 + 1) * g.k_blocks;  // end of the share's first tile
-    if (part == 1 && u1 <= edge) return false;
-    tile = g.whole + t0 + part;
-    p.kb0 = part == 0 ? u0 - t0 * g.k_blocks : 0;
-    p.kb1 = part == 0 ? (u1 < edge ? u1 - t0 * g.k_blocks : g.k_blocks) : u1 - edge;
-    p.slot = 2 * pair + part;
+    lin_tile(g, tile, p.mi, p.ni);
+    p.kb0 = 0;
+    p.kb1 = g.k_blocks;
+    p.slot = -1;
+    return true;
   }
-  p.mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
-  p.ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
+  const int item = (i - g.waves) * kLinPairs + pair;
+  if (item >= g.cut * g.parts) return false;
+  const int part = item / g.cut;
+  lin_tile(g, g.whole + item % g.cut, p.mi, p.ni);
+  p.kb0 = static_cast<int>(static_cast<long long>(g.k_blocks) * part / g.parts);
+  p.kb1 = static_cast<int>(static_cast<long long>(g.k_blocks) * (part + 1) / g.parts);
+  p.slot = item;
   return true;
 }
 
@@ -523,35 +521,31 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// The cut tiles: adds the shares' sums in the order of k and applies the
-// epilogue. One block takes 16 rows of one tile.
+// The cut tiles: adds the parts' sums in the order of k and applies the
+// epilogue. One block takes 8 rows of one tile.
 __global__ void __launch_bounds__(256) linear_finish_kernel(const LinGemmArgs g) {
   pdl_trigger();
   pdl_wait();
-  const int t = blockIdx.x;  // among the cut tiles
-  const int tile = g.whole + t;
-  const int mi = g.n_fastest ? tile / g.n_tiles : tile % g.m_tiles;
-  const int ni = g.n_fastest ? tile % g.n_tiles : tile / g.m_tiles;
+  int mi, ni;
+  lin_tile(g, g.whole + blockIdx.x, mi, ni);
   const int col = (threadIdx.x & 63) * 4;
   if (ni * 256 + col >= g.epi.n) return;
-  const int u0 = t * g.k_blocks, u1 = u0 + g.k_blocks;
-  // first and last share with part of this tile
-  int s0 = static_cast<int>(static_cast<long long>(u0) * g.shares / (static_cast<long long>(g.cut) * g.k_blocks));
-  while (s0 > 0 && lin_share(g, s0) > u0) --s0;
-  while (lin_share(g, s0 + 1) <= u0) ++s0;
   const float4 bias = lin_bias4(g.epi, ni * 256 + col);
-  for (int r = blockIdx.y * 16 + (threadIdx.x >> 6); r < blockIdx.y * 16 + 16; r += 4) {
+  const long long plane = static_cast<long long>(g.part_rows) * g.part_cols;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 6) + 4 * i;
     const long long row = static_cast<long long>(mi) * 256 + r;
     if (row >= g.epi.m) return;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = s0; s < g.shares && lin_share(g, s) < u1; ++s) {
-      const int slot = 2 * s + (lin_share(g, s) < u0 ? 1 : 0);  // the share began in the tile before
-      const float4 q = __ldcg(reinterpret_cast<const float4*>(
-          g.partial + (static_cast<long long>(slot) * g.part_rows + r) * g.part_cols + col));
-      v.x += q.x;
-      v.y += q.y;
-      v.z += q.z;
-      v.w += q.w;
+    const float* src = g.partial + blockIdx.x * plane + r * g.part_cols + col;
+    float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+#pragma unroll 4
+    for (int q = 1; q < g.parts; ++q) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(src + q * g.cut * plane));
+      v.x += t.x;
+      v.y += t.y;
+      v.z += t.z;
+      v.w += t.w;
     }
     lin_finish4(g.epi, row, ni * 256 + col, v, bias);
   }
@@ -735,9 +729,10 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, in
 // ------------------------------------------------------------------ host
 
 // How one product's tiles are dealt out, from its sizes alone (k already
-// counted twice where A has low halves). Costs in tensor-core clocks: a
-// 64-deep step of a 256 x 256 tile takes about 560; cutting the last wave's
-// tiles adds a second launch and the trip of every share's sums through L2.
+// counted twice where A has low halves). Costs in clocks at 1.9 GHz: a 64-deep
+// step of a 256 x 256 tile takes about 750 with all pairs at work, a part
+// 1500 more for filling and emptying its pipeline, the second launch 5000, and
+// the parts' sums go to L2 and back at about 4000 bytes per clock.
 LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   LinPlan p{};
   p.m_tiles = static_cast<int>((m + 255) / 256);
@@ -748,21 +743,24 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   p.whole = static_cast<int>(tiles);
   p.waves = static_cast<int>((tiles + kLinPairs - 1) / kLinPairs);
   const int rest = static_cast<int>(tiles % kLinPairs);
-  if (rest > 0) {
-    const long long units = rest * k_blocks;
-    long long shares = units / 4 < kLinPairs ? units / 4 : kLinPairs;  // at least 4 steps each
-    if (shares > rest) {
-      const double tile_bytes = 4.0 * p.part_rows * p.part_cols;
-      const double cut = static_cast<double>((units + shares - 1) / shares) * 560 + 6000 +
-                         2 * (shares + rest) * tile_bytes / 4000;
-      if (cut < static_cast<double>(k_blocks) * 560) {
-        p.cut = rest;
-        p.shares = static_cast<int>(shares);
-        p.whole = static_cast<int>(tiles) - rest;
-        p.waves = p.whole / kLinPairs;
-        p.partial_bytes = 2 * static_cast<size_t>(shares) * p.part_rows * p.part_cols * 4;
-      }
+  if (rest == 0) return p;
+  double best = 750.0 * k_blocks + 1500;
+  // at least 4 steps to a part, and at most two rounds of parts (more parts
+  // only add traffic)
+  for (long long parts = 2; parts * 4 <= k_blocks && rest * parts <= 2 * kLinPairs; ++parts) {
+    const long long rounds = (rest * parts + kLinPairs - 1) / kLinPairs;
+    const double bytes = 2.0 * rest * parts * p.part_rows * p.part_cols * 4;
+    const double cost = rounds * (750.0 * ((k_blocks + parts - 1) / parts) + 1500) + 5000 + bytes / 4000;
+    if (cost < best) {
+      best = cost;
+      p.cut = rest;
+      p.parts = static_cast<int>(parts);
     }
+  }
+  if (p.cut) {
+    p.whole = static_cast<int>(tiles) - rest;
+    p.waves = p.whole / kLinPairs;
+    p.partial_bytes = static_cast<size_t>(p.cut) * p.parts * p.part_rows * p.part_cols * 4;
   }
   return p;
 }
@@ -791,7 +789,8 @@ static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const Li
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return -1;
     pairs = n < kLinPairs ? n : kLinPairs;
   }
-  const int busy = g.waves > 0 ? (g.whole < kLinPairs ? g.whole : kLinPairs) : g.shares;
+  const int most = g.waves > 0 ? g.whole : g.cut * g.parts;
+  const int busy = most < kLinPairs ? most : kLinPairs;
   const int grid = busy < pairs ? busy : pairs;
   const cudaError_t e = launch_kernel(kernel, dim3(2 * grid), dim3(kLinThreads), kLinSmem, s, 2, ma, mb, g);
   note_launch();
@@ -821,7 +820,7 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
   g.waves = plan.waves;
   g.whole = plan.whole;
   g.cut = plan.cut;
-  g.shares = plan.shares;
+  g.parts = plan.parts;
   g.n_fastest = epi.n <= epi.m;  // the smaller operand stays in L2, the larger streams through once
   g.partial = partial;
   g.part_rows = plan.part_rows;
@@ -836,7 +835,7 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
     rc = epi.out_f32 ? launch_lin_one<true, true, true>(ma, mb, g, s) : launch_lin_one<true, true, false>(ma, mb, g, s);
   if (rc || !plan.cut) return rc;
   const cudaError_t e =
-      launch_kernel(linear_finish_kernel, dim3(plan.cut, (plan.part_rows + 15) / 16), dim3(256), 0, s, 1, g);
+      launch_kernel(linear_finish_kernel, dim3(plan.cut, (plan.part_rows + 7) / 8), dim3(256), 0, s, 1, g);
   note_launch();
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
