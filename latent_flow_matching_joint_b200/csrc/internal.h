@@ -19,6 +19,8 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t out
 // 3-D bf16 tensor map over [d2][d1][d0] with byte strides s1 (d1) and s2 (d2).
 int make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                 uint64_t s2, uint32_t box0, uint32_t box1, int bytes1 = 0);
+// 2-D map of rows of bf16 (or fp32) with pitch ld in elements; box 32 rows of 128 bytes, swizzled.
+int make_map_rows32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, int f32);
 // 4-D bf16 tensor map over [d3][d2][d1][d0] with byte strides s1..s3; box = box0 x box1 x 1 x 1.
 int make_map_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
                 uint64_t s2, uint64_t s3, uint32_t box0, uint32_t box1);
@@ -163,17 +165,18 @@ struct LinEpi {
   int act;
   int out_f32, res_f32;             // element types: fp32, else bf16
   int out_vec, res_vec, z_vec;      // four columns may be accessed at once (address and pitch allow it)
-  int vec;                          // ... of every matrix that there is
+  int tma;                          // set by launch_linear_gemm: out and res go by TMA, z in 16-byte pieces
 };
 
 struct LinGemmArgs {
   int m_tiles, n_tiles, k_blocks;
   int k_wrap, a_low;   // from step k_wrap on, A's columns a_low further on against B's from the start
   int waves, whole;    // the first `whole` tiles are dealt out whole, in `waves` rounds
+  int pairs;           // CTA pairs that the work is dealt out to
   int cut, parts;      // the last `cut` tiles are cut along k into `parts` equal parts each
   int n_fastest;       // number the tiles N-fastest instead of M-fastest
-  float* partial;      // [parts][cut][part_rows][part_cols] the parts' sums
-  int part_rows, part_cols;
+  float* partial;      // [parts][cut][part_rb][part_cb] boxes of 32 x 32, the parts' sums
+  int part_rb, part_cb;
   LinEpi epi;
 };
 
@@ -188,7 +191,7 @@ struct LinOperand {
 };
 
 struct LinPlan {
-  int m_tiles, n_tiles, waves, whole, cut, parts, part_rows, part_cols;
+  int m_tiles, n_tiles, waves, whole, cut, parts, part_rb, part_cb;
   size_t partial_bytes;  // workspace for the parts' sums, 0 if no tile is cut
 };
 LinPlan plan_linear(long long m, long long n, long long k_blocks);

@@ -144,6 +144,19 @@ int make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, ui
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
+int make_map_rows32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, int f32) {
+  if (get_encode()) return -1;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld * (f32 ? 4 : 2)};
+  cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = g_encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
 int make_map_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
                 uint64_t s2, uint64_t s3, uint32_t box0, uint32_t box1) {
   if (get_encode()) return -1;
@@ -1331,7 +1344,6 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
   e.z = static_cast<__nv_bfloat16*>(a->preact);
   e.z_ld = a->preact_ld;
   e.z_vec = vec4_ok(a->preact, a->preact_ld, 0);
-  e.vec = e.out_vec && (!e.res || e.res_vec) && (!e.z || e.z_vec);
   e.alpha = a->alpha;
   e.act = a->act;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1439,7 +1451,7 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     e.out = a->dx;
     e.out_ld = a->dx_ld;
     e.out_f32 = a->dx_f32 != 0;
-    e.vec = e.out_vec = vec4_ok(a->dx, a->dx_ld, e.out_f32);
+    e.out_vec = vec4_ok(a->dx, a->dx_ld, e.out_f32);
     dz.low = fine && e.out_f32 ? w.dz_cols : 0;
     rc = launch_linear_gemm(dz, {a->w, a->w_ld, 1, 0}, a->n, e, partial, s);
     if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -1451,7 +1463,7 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     e.out = a->dw;
     e.out_ld = a->dw_ld;
     e.out_f32 = a->dw_f32 != 0;
-    e.vec = e.out_vec = vec4_ok(a->dw, a->dw_ld, e.out_f32);
+    e.out_vec = vec4_ok(a->dw, a->dw_ld, e.out_f32);
     dz.mn_major = 1;
     dz.low = fine && e.out_f32 ? w.dz_cols : 0;
     rc = launch_linear_gemm(dz, {a->x, a->x_ld, 1, 0}, a->m, e, partial, s);

@@ -9,7 +9,7 @@
 // 128-byte-swizzled tiles, and the MMA's operand descriptors and major bits
 // read either, so no transposed copy of anything is made.
 //
-// linear_gemm_kernel: persistent CTA pairs, 256 x 256 output tiles, 6 x 32 KB
+// linear_gemm_kernel: persistent CTA pairs, 256 x 256 output tiles, 5 x 32 KB
 // ring, 384 threads: warp 0 TMA, warp 1 MMA issue, warps 4..11 epilogue (two
 // per TMEM lane quarter, half of the tile's columns each), two TMEM accumulators so
 // that a tile's epilogue overlaps the next one's main loop.
@@ -41,9 +41,10 @@ namespace {
 
 constexpr int kLinTile = 128 * 64 * 2;         // one operand tile: 128 rows (or columns) x 64 k, bf16
 constexpr int kLinStage = 2 * kLinTile;        // A and B
-constexpr int kLinStages = 6;
+constexpr int kLinStages = 5;
 constexpr int kLinRing = kLinStages * kLinStage;
-constexpr int kLinStaging = 8 * 4096;          // per epilogue warp: 32 rows x 32 fp32 columns
+constexpr int kLinBox = 4096;                  // 32 rows of 128 bytes: 32 columns of fp32 or 64 of bf16
+constexpr int kLinStaging = 8 * 2 * kLinBox;   // two per epilogue warp
 constexpr int kLinSmem = kLinRing + kLinStaging + 256 + 1024;
 constexpr int kLinThreads = 384;
 constexpr int kLinChunk = 8;                   // FINE: k blocks (of 64) per TMEM accumulation
@@ -165,7 +166,7 @@ __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
 }  // namespace
 
 // A pair's share of the work: for w < waves the whole tile w * pairs + pair,
-// then every kLinPairs-th of the cut tiles' parts.
+// then every pairs-th of the cut tiles' parts.
 struct LinPiece {
   int mi, ni, kb0, kb1;
   int slot;  // where its sums go in the workspace, or -1: a whole tile, finished here
@@ -178,7 +179,7 @@ __device__ __forceinline__ void lin_tile(const LinGemmArgs& g, int tile, int& mi
 
 __device__ __forceinline__ bool lin_piece(const LinGemmArgs& g, int pair, int i, LinPiece& p) {
   if (i < g.waves) {
-    const int tile = i * kLinPairs + pair;
+    const int tile = i * g.pairs + pair;
     if (tile >= g.whole) return false;
     lin_tile(g, tile, p.mi, p.ni);
     p.kb0 = 0;
@@ -186,7 +187,7 @@ __device__ __forceinline__ bool lin_piece(const LinGemmArgs& g, int pair, int i,
     p.slot = -1;
     return true;
   }
-  const int item = (i - g.waves) * kLinPairs + pair;
+  const int item = (i - g.waves) * g.pairs + pair;
   if (item >= g.cut * g.parts) return false;
   const int part = item / g.cut;
   lin_tile(g, g.whole + item % g.cut, p.mi, p.ni);
@@ -196,99 +197,106 @@ __device__ __forceinline__ bool lin_piece(const LinGemmArgs& g, int pair, int i,
   return true;
 }
 
-// Epilogue of ROWS rows (rr = 4 r + sub, r < ROWS) x 4 columns per lane of a
-// warp's 32 x 32 piece, whose sums lie in shared memory.
-template <int ROWS>
-__device__ __forceinline__ void lin_finish_block(const LinEpi& e, const float* stg, int r0, long long row0, int col,
-                                                 int sub, int c4) {
-  float4 v[ROWS];
-  float4 res[ROWS];
-  const int rows_left = static_cast<int>(e.m - row0 < 32 ? e.m - row0 : 32);
-  const bool vec = e.vec && col + 4 <= e.n;
-  if (!vec) {  // odd widths, pitches and addresses: element by element
-    const float4 bias = lin_bias4(e, col);
-#pragma unroll 1
-    for (int r = 0; r < ROWS; ++r) {
-      const int rr = 4 * (r0 + r) + sub;
-      if (rr < rows_left && col < e.n)
-        lin_finish4(e, row0 + rr, col, *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2)), bias);
-    }
-    return;
+// ---- the epilogue's boxes: 32 rows of 128 bytes in shared memory, one row per
+// lane, 16-byte pieces swizzled the way TMA does it (by row % 8), so that neither
+// a lane's own row nor whole rows conflict.
+
+__device__ __forceinline__ uint8_t* lin_piece16(uint8_t* box, int row, int i) {
+  return box + row * 128 + ((i ^ (row & 7)) << 4);
+}
+
+// 32 columns of one row: all of a box of fp32, or half (0, 1) of one of bf16.
+__device__ __forceinline__ void lin_box_write(uint8_t* box, int row, const float* v, bool f32, int half) {
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float4*>(lin_piece16(box, row, i)) =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(lin_piece16(box, row, 4 * half + i)) =
+          make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                     pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
   }
-  if (e.res) {  // all of them in flight at once
-    if (e.res_f32) {
+}
+
+// v += those columns
+__device__ __forceinline__ void lin_box_add(uint8_t* box, int row, float* v, bool f32, int half) {
+  if (f32) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const int rr = 4 * (r0 + r) + sub;
-        if (rr < rows_left)
-          res[r] = *reinterpret_cast<const float4*>(static_cast<const float*>(e.res) + (row0 + rr) * e.res_ld + col);
-      }
-    } else {
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const int rr = 4 * (r0 + r) + sub;
-        if (rr < rows_left) {
-          const uint2 t =
-              *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.res) + (row0 + rr) * e.res_ld + col);
-          const float2 lo = unpack_bf16(t.x), hi = unpack_bf16(t.y);
-          res[r] = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int rr = 4 * (r0 + r) + sub;
-    v[r] = *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2));
-  }
-  if (e.bias) {
-    const float4 bias = lin_bias4(e, col);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      v[r].x += bias.x;
-      v[r].y += bias.y;
-      v[r].z += bias.z;
-      v[r].w += bias.w;
-    }
-  }
-  if (e.z) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int rr = 4 * (r0 + r) + sub;
-      if (rr < rows_left)
-        *reinterpret_cast<uint2*>(e.z + (row0 + rr) * e.z_ld + col) =
-            make_uint2(pack_bf16(v[r].x, v[r].y), pack_bf16(v[r].z, v[r].w));
-    }
-  }
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      v[r].x = lin_act(v[r].x, e.act);
-      v[r].y = lin_act(v[r].y, e.act);
-      v[r].z = lin_act(v[r].z, e.act);
-      v[r].w = lin_act(v[r].w, e.act);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const float4 t = e.res ? res[r] : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[r] = make_float4(fmaf(e.alpha, v[r].x, t.x), fmaf(e.alpha, v[r].y, t.y), fmaf(e.alpha, v[r].z, t.z),
-                       fmaf(e.alpha, v[r].w, t.w));
-  }
-  if (e.out_f32) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int rr = 4 * (r0 + r) + sub;
-      if (rr < rows_left)
-        *reinterpret_cast<float4*>(static_cast<float*>(e.out) + (row0 + rr) * e.out_ld + col) = v[r];
+    for (int i = 0; i < 8; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(lin_piece16(box, row, i));
+      v[4 * i] += t.x;
+      v[4 * i + 1] += t.y;
+      v[4 * i + 2] += t.z;
+      v[4 * i + 3] += t.w;
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int rr = 4 * (r0 + r) + sub;
-      if (rr < rows_left)
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.out) + (row0 + rr) * e.out_ld + col) =
-            make_uint2(pack_bf16(v[r].x, v[r].y), pack_bf16(v[r].z, v[r].w));
+    for (int i = 0; i < 4; ++i) {
+      const uint4 t = *reinterpret_cast<const uint4*>(lin_piece16(box, row, 4 * half + i));
+      const uint32_t u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack_bf16(u[j]);
+        v[8 * i + 2 * j] += f.x;
+        v[8 * i + 2 * j + 1] += f.y;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void lin_bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// until the bulk stores of this thread have read their shared memory / are done
+__device__ __forceinline__ void lin_bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void lin_bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void lin_store_box(const CUtensorMap* map, const void* box, int col, int row) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(box)), "r"(col), "r"(row)
+               : "memory");
+}
+
+__device__ __forceinline__ void lin_store_raw(void* dst, const void* box, int bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(box)), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void lin_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The epilogue element by element: this lane's column of a box of fp32 sums,
+// 32 rows from row0 on. Any pitch, width and alignment; a row's 32 elements
+// are one access of the warp. Eight rows' residuals are in flight at a time.
+__device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t* box, int lane, long long row0,
+                                                  int col0) {
+  const int col = col0 + lane;
+  const int rows = static_cast<int>(e.m - row0 < 32 ? e.m - row0 : 32);
+  if (col >= e.n) return;
+  const float bias = e.bias ? __ldg(e.bias + col) : 0.f;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    float z[8], res[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + i;
+      z[i] = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) + bias;
+      res[i] = e.res && r < rows ? lin_load(e.res, (row0 + r) * e.res_ld + col, e.res_f32) : 0.f;
+    }
+    if (e.z) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r0 + i < rows) e.z[(row0 + r0 + i) * e.z_ld + col] = __float2bfloat16_rn(z[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= rows) break;
+      const float y = fmaf(e.alpha, lin_act(z[i], e.act), res[i]);
+      const long long o = (row0 + r0 + i) * e.out_ld + col;
+      if (e.out_f32) static_cast<float*>(e.out)[o] = y;
+      else static_cast<__nv_bfloat16*>(e.out)[o] = __float2bfloat16_rn(y);
     }
   }
 }
@@ -296,6 +304,7 @@ __device__ __forceinline__ void lin_finish_block(const LinEpi& e, const float* s
 template <bool AMN, bool BMN, bool FINE>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_res,
                        const LinGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -304,7 +313,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint64_t* acc_full = empty + kLinStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* res_full = drain + 1;  // [8 epilogue warps]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 8);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -321,9 +331,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(&acc_empty[a], 16);  // one arrival per epilogue warp of the pair
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&res_full[i], 1);
     fence_barrier_init();
     tma_prefetch_desc(&map_a);
     tma_prefetch_desc(&map_b);
+    if (g.epi.tma) {
+      tma_prefetch_desc(&map_out);
+      if (g.epi.res) tma_prefetch_desc(&map_res);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -341,14 +356,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   LinPiece p;
 
   if (warp < 4) {
-    if (FINE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       StageLog log;
       bool ok = true;
-      for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+      for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
         for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
           const int row = p.mi * 256 + 128 * rank, col = p.ni * 256 + 128 * rank;
           for (int kb = p.kb0; kb < p.kb1; ++kb) {
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t phase = 0;
       int chunk = 0;
       bool ok = true;
-      for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+      for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
         for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
           for (int kb = p.kb0; ok && kb < p.kb1; ++chunk) {
             const int acc = chunk & 1;
@@ -423,11 +438,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     }
   } else {
-    if (FINE) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;
     const int part = (warp - 4) >> 2;  // which half of the tile's columns
-    float* stg = reinterpret_cast<float*>(smem + kLinRing + (warp - 4) * 4096);
-    const int sub = lane >> 3, c4 = lane & 7;  // after the transposition: rows 4 r + sub, columns 4 c4..4 c4 + 3
+    const LinEpi& e = g.epi;
+    uint8_t* boxes = smem + kLinRing + (warp - 4) * 2 * kLinBox;
+    uint64_t* rbar = res_full + (warp - 4);
+    const bool load_res = e.tma && e.res;
+    // A round is what the two boxes hold: 128 columns if everything is bf16, else 64.
+    const bool wide = e.tma && !e.out_f32 && !(e.res && e.res_f32);
+    const int round_cols = wide ? 128 : 64;
+    uint32_t res_phase = 0;  // parity of the next residual
+    bool res_due = false;    // lane 0: a residual is on its way
     int chunk = 0;
     bool ok = true;
     auto release = [&](int buf) {
@@ -435,37 +457,105 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     };
-    // Each thread holds one row; through shared memory (16-byte chunks,
-    // XOR-swizzled by row) a warp's 32 x 32 piece turns into row segments,
-    // so that residual reads and output writes fill their sectors.
-    auto finish = [&](const float* v, int row0, int col0) {
+    auto fetch_res = [&](int row0, int col) {  // lane 0: a round's residual, into boxes that nothing uses
+      lin_bulk_wait_read();
+      const int per_box = e.res_f32 ? 32 : 64;
+      const bool two = (wide || e.res_f32) && col + per_box < e.n;
+      mbar_arrive_expect_tx(rbar, two ? 2 * kLinBox : kLinBox);
+      res_due = true;
+      tma_load_2d(boxes + (e.out_f32 && !e.res_f32 ? kLinBox : 0), &map_res, rbar, col, row0);
+      if (two) tma_load_2d(boxes + kLinBox, &map_res, rbar, col + per_box, row0);
+    };
+    // The boxes as they stand become the round's columns of the output.
+    auto store_round = [&](int per_box, int cols, int row0, int col) {
+      lin_fence_async();
       __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<float4*>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) =
-            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      __syncwarp();
-      if (p.slot >= 0) {
-        float* dst = g.partial + (static_cast<long long>(p.slot) * g.part_rows + (row0 - p.mi * 256)) * g.part_cols +
-                     (col0 - p.ni * 256) + 4 * c4;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int rr = 4 * r + sub;
-          if (row0 + rr < g.epi.m)
-            *reinterpret_cast<float4*>(dst + rr * g.part_cols) =
-                *reinterpret_cast<const float4*>(stg + rr * 32 + ((c4 ^ (rr & 7)) << 2));
-        }
-      } else if (FINE) {
-        lin_finish_block<4>(g.epi, stg, 0, row0, col0 + 4 * c4, sub, c4);
-        lin_finish_block<4>(g.epi, stg, 4, row0, col0 + 4 * c4, sub, c4);
-      } else {
-        lin_finish_block<8>(g.epi, stg, 0, row0, col0 + 4 * c4, sub, c4);
+      if (lane == 0) {
+        lin_store_box(&map_out, boxes, col, row0);
+        if (cols > per_box && col + per_box < e.n) lin_store_box(&map_out, boxes + kLinBox, col + per_box, row0);
+        lin_bulk_commit();
       }
     };
-    for (int pair = pair0; ok && pair < kLinPairs; pair += pairs) {
+    auto boxes_free = [&]() {
+      if (lane == 0) lin_bulk_wait_read();
+      __syncwarp();
+    };
+    // 32 columns q of the tile half at col0; v: this lane's row; last: no more columns in the matrix. One copy of
+    // this code, and its loop rolled up: unrolled for all 128 columns it no longer fits the instruction cache, which
+    // made the epilogue three times slower.
+    auto finish = [&](float* v, int q, int row0, int col0, bool last) {
+      const int col = col0 + 32 * q;
+      if (p.slot >= 0) {  // a part's sums, as the boxes are
+        if ((q & 1) == 0) boxes_free();
+        lin_box_write(boxes + (q & 1) * kLinBox, lane, v, true, 0);
+        if ((q & 1) || last) {
+          lin_fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            const int rb = 4 * rank + quarter, cb = 4 * part + (q & 2);
+            lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
+                          boxes, (q & 1) ? 2 * kLinBox : kLinBox);
+            lin_bulk_commit();
+          }
+        }
+        return;
+      }
+      if (!e.tma) {  // pitches, widths or addresses that TMA cannot take: a column to a lane, row by row
+        __syncwarp();
+        lin_box_write(boxes, lane, v, true, 0);
+        __syncwarp();
+        lin_finish_column(e, boxes, lane, row0, col);
+        return;
+      }
+      if (e.bias) {
+        const float bias = col + lane < e.n ? __ldg(e.bias + col + lane) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+      }
+      if (e.z && row0 + lane < e.m) {  // two whole sectors of this lane's row
+        __nv_bfloat16* zp = e.z + (row0 + lane) * e.z_ld + col;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (col + i < e.n)
+            *reinterpret_cast<uint4*>(zp + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                                                           pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+      }
+      if (e.act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActSilu);
+      } else if (e.act == kActGelu) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActGelu);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= e.alpha;
+      const int at = (32 * q) & (round_cols - 1);  // within the round
+      const bool first = at == 0;
+      if (load_res) {
+        if (first) {
+          if (!mbar_wait(rbar, res_phase, 0x307)) { ok = false; return; }
+          res_phase ^= 1;
+          res_due = false;
+        }
+        // (64 columns of a bf16 residual lie in the box that the second 32 of an fp32 output take)
+        lin_box_add(boxes + (e.res_f32 ? at >> 5 : (e.out_f32 ? 1 : at >> 6)) * kLinBox, lane, v, e.res_f32,
+                    (at >> 5) & 1);
+      } else if (first) {
+        boxes_free();
+      }
+      lin_box_write(boxes + (e.out_f32 ? at >> 5 : at >> 6) * kLinBox, lane, v, e.out_f32, (at >> 5) & 1);
+      if (last || at + 32 == round_cols) {
+        store_round(e.out_f32 ? 32 : 64, at + 32, row0, col - at);
+        if (load_res && !last && lane == 0) fetch_res(row0, col + 32);
+      }
+    };
+    for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
       for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
         const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
         const int col0 = p.ni * 256 + part * 128;
+        int blocks = row0 < e.m && col0 < e.n ? (e.n - col0 + 31) / 32 : 0;  // of 32 columns
+        if (blocks > 4) blocks = 4;
+        if (load_res && p.slot < 0 && lane == 0 && blocks > 0) fetch_res(row0, col0);  // during the main loop
         if (FINE) {
           const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
           float acc[128];
@@ -488,10 +578,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             release(buf);
           }
-          if (!ok) break;
+#pragma unroll 1
+          for (int q = 0; ok && q < blocks; ++q) {
+            float v[32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row0 < g.epi.m && col0 + 32 * j < g.epi.n) finish(acc + 32 * j, row0, col0 + 32 * j);
+            for (int j = 0; j < 32; ++j) {
+              const float lo = q & 1 ? acc[32 + j] : acc[j], hi = q & 1 ? acc[96 + j] : acc[64 + j];
+              v[j] = q & 2 ? hi : lo;
+            }
+            finish(v, q, row0, col0, q == blocks - 1);
+          }
         } else {
           const int buf = chunk & 1;
           if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
@@ -499,15 +595,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tc_fence_after();
           const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            if (row0 >= g.epi.m || col0 + 32 * j >= g.epi.n) break;
+          for (int q = 0; ok && q < blocks; ++q) {
             float v[32];
-            tmem_ld32(taddr + 32 * j, v);
-            finish(v, row0, col0 + 32 * j);
+            tmem_ld32(taddr + 32 * q, v);
+            if (q == blocks - 1) release(buf);
+            finish(v, q, row0, col0, q == blocks - 1);
           }
-          release(buf);
+          if (blocks == 0) release(buf);
         }
       }
+    }
+    if (lane == 0) {
+      // when the CTA exits no store may still read shared memory, and (after a
+      // wait that gave up) no residual may still be on its way
+      lin_bulk_wait_all();
+      if (res_due) mbar_wait(rbar, res_phase, 0x308);
     }
   }
 
@@ -522,33 +624,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 // The cut tiles: adds the parts' sums in the order of k and applies the
-// epilogue. One block takes 8 rows of one tile.
+// epilogue. One block takes one 32 x 32 box of a tile, a float4 per thread.
 __global__ void __launch_bounds__(256) linear_finish_kernel(const LinGemmArgs g) {
   pdl_trigger();
   pdl_wait();
   int mi, ni;
-  lin_tile(g, g.whole + blockIdx.x, mi, ni);
-  const int col = (threadIdx.x & 63) * 4;
-  if (ni * 256 + col >= g.epi.n) return;
-  const float4 bias = lin_bias4(g.epi, ni * 256 + col);
-  const long long plane = static_cast<long long>(g.part_rows) * g.part_cols;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 6) + 4 * i;
-    const long long row = static_cast<long long>(mi) * 256 + r;
-    if (row >= g.epi.m) return;
-    const float* src = g.partial + blockIdx.x * plane + r * g.part_cols + col;
-    float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+  lin_tile(g, g.whole + blockIdx.y, mi, ni);
+  const int rb = blockIdx.x / g.part_cb, cb = blockIdx.x % g.part_cb;
+  const int r = threadIdx.x >> 3, c4 = threadIdx.x & 7;
+  const long long row = static_cast<long long>(mi) * 256 + rb * 32 + r;
+  const int col = ni * 256 + cb * 32 + c4 * 4;
+  if (row >= g.epi.m || col >= g.epi.n) return;
+  const long long plane = static_cast<long long>(g.part_rb) * g.part_cb * (kLinBox / 4);
+  const float* src = g.partial + blockIdx.y * plane + static_cast<long long>(blockIdx.x) * (kLinBox / 4) + r * 32 +
+                     ((c4 ^ (r & 7)) << 2);
+  float4 v = __ldcg(reinterpret_cast<const float4*>(src));
 #pragma unroll 4
-    for (int q = 1; q < g.parts; ++q) {
-      const float4 t = __ldcg(reinterpret_cast<const float4*>(src + q * g.cut * plane));
-      v.x += t.x;
-      v.y += t.y;
-      v.z += t.z;
-      v.w += t.w;
-    }
-    lin_finish4(g.epi, row, ni * 256 + col, v, bias);
+  for (int q = 1; q < g.parts; ++q) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(src + q * g.cut * plane));
+    v.x += t.x;
+    v.y += t.y;
+    v.z += t.z;
+    v.w += t.w;
   }
+  lin_finish4(g.epi, row, col, v, lin_bias4(g.epi, col));
 }
 
 // Few rows (m <= MV <= 4): the weights are read once, straight into registers,
@@ -738,8 +837,8 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   p.m_tiles = static_cast<int>((m + 255) / 256);
   p.n_tiles = static_cast<int>((n + 255) / 256);
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
-  p.part_rows = static_cast<int>(m < 256 ? m : 256);
-  p.part_cols = static_cast<int>(n < 256 ? (n + 31) / 32 * 32 : 256);
+  p.part_rb = static_cast<int>(m < 256 ? (m + 31) / 32 : 8);
+  p.part_cb = static_cast<int>(n < 256 ? (n + 31) / 32 : 8);
   p.whole = static_cast<int>(tiles);
   p.waves = static_cast<int>((tiles + kLinPairs - 1) / kLinPairs);
   const int rest = static_cast<int>(tiles % kLinPairs);
@@ -749,7 +848,7 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   // only add traffic)
   for (long long parts = 2; parts * 4 <= k_blocks && rest * parts <= 2 * kLinPairs; ++parts) {
     const long long rounds = (rest * parts + kLinPairs - 1) / kLinPairs;
-    const double bytes = 2.0 * rest * parts * p.part_rows * p.part_cols * 4;
+    const double bytes = 2.0 * rest * parts * p.part_rb * p.part_cb * kLinBox;
     const double cost = rounds * (750.0 * ((k_blocks + parts - 1) / parts) + 1500) + 5000 + bytes / 4000;
     if (cost < best) {
       best = cost;
@@ -760,13 +859,14 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   if (p.cut) {
     p.whole = static_cast<int>(tiles) - rest;
     p.waves = p.whole / kLinPairs;
-    p.partial_bytes = static_cast<size_t>(p.cut) * p.parts * p.part_rows * p.part_cols * 4;
+    p.partial_bytes = static_cast<size_t>(p.cut) * p.parts * p.part_rb * p.part_cb * kLinBox;
   }
   return p;
 }
 
 template <bool AMN, bool BMN, bool FINE>
-static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const LinGemmArgs& g, cudaStream_t s) {
+static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CUtensorMap& mr,
+                          const LinGemmArgs& g, cudaStream_t s) {
   static int pairs_dev[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return -1;
@@ -789,12 +889,18 @@ static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const Li
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return -1;
     pairs = n < kLinPairs ? n : kLinPairs;
   }
-  const int most = g.waves > 0 ? g.whole : g.cut * g.parts;
-  const int busy = most < kLinPairs ? most : kLinPairs;
-  const int grid = busy < pairs ? busy : pairs;
-  const cudaError_t e = launch_kernel(kernel, dim3(2 * grid), dim3(kLinThreads), kLinSmem, s, 2, ma, mb, g);
+  const int grid = g.pairs < pairs ? g.pairs : pairs;
+  const cudaError_t e = launch_kernel(kernel, dim3(2 * grid), dim3(kLinThreads), kLinSmem, s, 2, ma, mb, mo, mr, g);
   note_launch();
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
+}
+
+// Whether TMA can take a matrix's rows: 16-byte aligned address and pitch, and
+// a width of whole 16-byte pieces (a store clips a row to those: past an odd
+// width it would write zeros).
+static bool tma_rows_ok(const void* p, long long ld, long long n, int f32) {
+  const int size = f32 ? 4 : 2;
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16 == 0 && (n * size) % 16 == 0;
 }
 
 int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const LinEpi& epi, float* partial,
@@ -822,20 +928,29 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
   g.cut = plan.cut;
   g.parts = plan.parts;
   g.n_fastest = epi.n <= epi.m;  // the smaller operand stays in L2, the larger streams through once
+  const int most = plan.waves > 0 ? plan.whole : plan.cut * plan.parts;
+  g.pairs = most < kLinPairs ? most : kLinPairs;
   g.partial = partial;
-  g.part_rows = plan.part_rows;
-  g.part_cols = plan.part_cols;
+  g.part_rb = plan.part_rb;
+  g.part_cb = plan.part_cb;
   g.epi = epi;
+  CUtensorMap mo = ma, mr = ma;  // not read unless epi.tma
+  g.epi.tma = tma_rows_ok(epi.out, epi.out_ld, epi.n, epi.out_f32) &&
+              (!epi.res || tma_rows_ok(epi.res, epi.res_ld, epi.n, epi.res_f32)) &&
+              (!epi.z || tma_rows_ok(epi.z, epi.z_ld, epi.n, 0));
+  if (g.epi.tma && (make_map_rows32(&mo, epi.out, epi.n, epi.m, epi.out_ld, epi.out_f32) ||
+                    (epi.res && make_map_rows32(&mr, epi.res, epi.n, epi.m, epi.res_ld, epi.res_f32))))
+    return -2;
   int rc;
   if (!a.mn_major && !b.mn_major)
-    rc = epi.out_f32 ? launch_lin_one<false, false, true>(ma, mb, g, s) : launch_lin_one<false, false, false>(ma, mb, g, s);
+    rc = epi.out_f32 ? launch_lin_one<false, false, true>(ma, mb, mo, mr, g, s) : launch_lin_one<false, false, false>(ma, mb, mo, mr, g, s);
   else if (!a.mn_major)
-    rc = epi.out_f32 ? launch_lin_one<false, true, true>(ma, mb, g, s) : launch_lin_one<false, true, false>(ma, mb, g, s);
+    rc = epi.out_f32 ? launch_lin_one<false, true, true>(ma, mb, mo, mr, g, s) : launch_lin_one<false, true, false>(ma, mb, mo, mr, g, s);
   else
-    rc = epi.out_f32 ? launch_lin_one<true, true, true>(ma, mb, g, s) : launch_lin_one<true, true, false>(ma, mb, g, s);
+    rc = epi.out_f32 ? launch_lin_one<true, true, true>(ma, mb, mo, mr, g, s) : launch_lin_one<true, true, false>(ma, mb, mo, mr, g, s);
   if (rc || !plan.cut) return rc;
   const cudaError_t e =
-      launch_kernel(linear_finish_kernel, dim3(plan.cut, (plan.part_rows + 7) / 8), dim3(256), 0, s, 1, g);
+      launch_kernel(linear_finish_kernel, dim3(plan.part_rb * plan.part_cb, plan.cut), dim3(256), 0, s, 1, g);
   note_launch();
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
