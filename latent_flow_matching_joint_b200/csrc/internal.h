@@ -197,7 +197,7 @@ struct LinPlan {
 LinPlan plan_linear(long long m, long long n, long long k_blocks);
 
 // The product and its epilogue (one or two launches). A row-contiguous only
-// together with B. Returns 0, -1 (launch) or -2 (tensor map).
+// together with B; bias, z and activation only with both k-contiguous. Returns 0, -1 (launch) or -2 (tensor map).
 int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const LinEpi& epi, float* partial,
                        cudaStream_t stream);
 // The same for at most 4 rows of k-contiguous operands, without tensor cores.

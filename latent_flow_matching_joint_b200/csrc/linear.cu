@@ -270,38 +270,68 @@ __device__ __forceinline__ void lin_fence_async() { asm volatile("fence.proxy.as
 // The epilogue element by element: this lane's column of a box of fp32 sums,
 // 32 rows from row0 on. Any pitch, width and alignment; a row's 32 elements
 // are one access of the warp. Eight rows' residuals are in flight at a time.
-__device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t* box, int lane, long long row0,
-                                                  int col0) {
-  const int col = col0 + lane;
-  const int rows = static_cast<int>(e.m - row0 < 32 ? e.m - row0 : 32);
+template <bool OUT32, bool FULL>
+__device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t* box, int lane, int row0, int col) {
+  const int rows = e.m - row0 < 32 ? e.m - row0 : 32;
   if (col >= e.n) return;
-  const float bias = e.bias ? __ldg(e.bias + col) : 0.f;
+  const float bias = FULL && e.bias ? __ldg(e.bias + col) : 0.f;
+  const long long out_ld = e.out_ld, res_ld = e.res_ld, z_ld = e.z_ld;
+  float* o32 = static_cast<float*>(e.out) + row0 * out_ld + col;
+  __nv_bfloat16* o16 = static_cast<__nv_bfloat16*>(e.out) + row0 * out_ld + col;
+  const float* r32 = static_cast<const float*>(e.res) + row0 * res_ld + col;
+  const __nv_bfloat16* r16 = static_cast<const __nv_bfloat16*>(e.res) + row0 * res_ld + col;
+  __nv_bfloat16* z16 = e.z + row0 * z_ld + col;
+  const bool has_res = e.res != nullptr, res_f32 = e.res_f32, has_z = FULL && e.z != nullptr;
+  const float alpha = e.alpha;
+  const int act = FULL ? e.act : kActNone;
+  const uint8_t* src = box + (lane & 3) * 4;
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += 8) {
     float z[8], res[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + i;
-      z[i] = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) + bias;
-      res[i] = e.res && r < rows ? lin_load(e.res, (row0 + r) * e.res_ld + col, e.res_f32) : 0.f;
+      z[i] = *reinterpret_cast<const float*>(src + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4)) + bias;
+      res[i] = 0.f;
     }
-    if (e.z) {
+    if (has_res) {
+      if (res_f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < rows) res[i] = r32[i * res_ld];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < rows) res[i] = __bfloat162float(r16[i * res_ld]);
+      }
+      r32 += 8 * res_ld;
+      r16 += 8 * res_ld;
+    }
+    if (has_z) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (r0 + i < rows) e.z[(row0 + r0 + i) * e.z_ld + col] = __float2bfloat16_rn(z[i]);
+        if (r0 + i < rows) z16[i * z_ld] = __float2bfloat16_rn(z[i]);
+      z16 += 8 * z_ld;
+    }
+    if (act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = lin_act(z[i], act);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (r0 + i >= rows) break;
-      const float y = fmaf(e.alpha, lin_act(z[i], e.act), res[i]);
-      const long long o = (row0 + r0 + i) * e.out_ld + col;
-      if (e.out_f32) static_cast<float*>(e.out)[o] = y;
-      else static_cast<__nv_bfloat16*>(e.out)[o] = __float2bfloat16_rn(y);
+      const float y = fmaf(alpha, z[i], res[i]);
+      if (r0 + i < rows) {
+        if (OUT32) o32[i * out_ld] = y;
+        else o16[i * out_ld] = __float2bfloat16_rn(y);
+      }
     }
+    o32 += 8 * out_ld;
+    o16 += 8 * out_ld;
   }
 }
 
-template <bool AMN, bool BMN, bool FINE>
+// FINE: the output is fp32. FULL: the epilogue may have a bias, a saved
+// pre-activation and an activation (the products of the backward pass never do).
+template <bool AMN, bool BMN, bool FINE, bool FULL>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_res,
@@ -444,10 +474,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const LinEpi& e = g.epi;
     uint8_t* boxes = smem + kLinRing + (warp - 4) * 2 * kLinBox;
     uint64_t* rbar = res_full + (warp - 4);
-    const bool load_res = e.tma && e.res;
+    // What the epilogue asks of its arguments again and again, asked once.
+    const bool tma = e.tma, has_bias = FULL && e.bias != nullptr, has_z = FULL && e.z != nullptr;
+    const bool load_res = tma && e.res, res32 = e.res_f32;
+    const int act = FULL ? e.act : kActNone;
+    const float alpha = e.alpha;
+    const int m = e.m, n = e.n;
     // A round is what the two boxes hold: 128 columns if everything is bf16, else 64.
-    const bool wide = e.tma && !e.out_f32 && !(e.res && e.res_f32);
-    const int round_cols = wide ? 128 : 64;
+    const bool wide = !FINE && !(load_res && res32);
     uint32_t res_phase = 0;  // parity of the next residual
     bool res_due = false;    // lane 0: a residual is on its way
     int chunk = 0;
@@ -459,103 +493,119 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     };
     auto fetch_res = [&](int row0, int col) {  // lane 0: a round's residual, into boxes that nothing uses
       lin_bulk_wait_read();
-      const int per_box = e.res_f32 ? 32 : 64;
-      const bool two = (wide || e.res_f32) && col + per_box < e.n;
+      const int per_box = res32 ? 32 : 64;
+      const bool two = (wide || res32) && col + per_box < n;
       mbar_arrive_expect_tx(rbar, two ? 2 * kLinBox : kLinBox);
       res_due = true;
-      tma_load_2d(boxes + (e.out_f32 && !e.res_f32 ? kLinBox : 0), &map_res, rbar, col, row0);
+      // (64 columns of bf16 lie in the second box if the output is fp32: the lane reads them all before it writes)
+      tma_load_2d(boxes + (FINE && !res32 ? kLinBox : 0), &map_res, rbar, col, row0);
       if (two) tma_load_2d(boxes + kLinBox, &map_res, rbar, col + per_box, row0);
-    };
-    // The boxes as they stand become the round's columns of the output.
-    auto store_round = [&](int per_box, int cols, int row0, int col) {
-      lin_fence_async();
-      __syncwarp();
-      if (lane == 0) {
-        lin_store_box(&map_out, boxes, col, row0);
-        if (cols > per_box && col + per_box < e.n) lin_store_box(&map_out, boxes + kLinBox, col + per_box, row0);
-        lin_bulk_commit();
-      }
     };
     auto boxes_free = [&]() {
       if (lane == 0) lin_bulk_wait_read();
       __syncwarp();
     };
-    // 32 columns q of the tile half at col0; v: this lane's row; last: no more columns in the matrix. One copy of
-    // this code, and its loop rolled up: unrolled for all 128 columns it no longer fits the instruction cache, which
-    // made the epilogue three times slower.
-    auto finish = [&](float* v, int q, int row0, int col0, bool last) {
-      const int col = col0 + 32 * q;
+    // The boxes as they stand become columns col..col + cols - 1 of the output.
+    auto store_boxes = [&](int cols, int row0, int col) {
+      constexpr int per_box = FINE ? 32 : 64;
+      lin_fence_async();
+      __syncwarp();
+      if (lane == 0) {
+        lin_store_box(&map_out, boxes, col, row0);
+        if (cols > per_box && col + per_box < n) lin_store_box(&map_out, boxes + kLinBox, col + per_box, row0);
+        lin_bulk_commit();
+      }
+    };
+    // 64 columns (half h of the tile half at col0); v: this lane's row; last: no more columns in the matrix.
+    auto finish = [&](float* v, int h, int row0, int col0, bool last) {
+      const int col = col0 + 64 * h;
       if (p.slot >= 0) {  // a part's sums, as the boxes are
-        if ((q & 1) == 0) boxes_free();
-        lin_box_write(boxes + (q & 1) * kLinBox, lane, v, true, 0);
-        if ((q & 1) || last) {
-          lin_fence_async();
-          __syncwarp();
-          if (lane == 0) {
-            const int rb = 4 * rank + quarter, cb = 4 * part + (q & 2);
-            lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
-                          boxes, (q & 1) ? 2 * kLinBox : kLinBox);
-            lin_bulk_commit();
-          }
+        boxes_free();
+        lin_box_write(boxes, lane, v, true, 0);
+        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
+        lin_fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          const int rb = 4 * rank + quarter, cb = 4 * part + 2 * h;
+          lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
+                        boxes, cb + 1 < g.part_cb ? 2 * kLinBox : kLinBox);
+          lin_bulk_commit();
         }
         return;
       }
-      if (!e.tma) {  // pitches, widths or addresses that TMA cannot take: a column to a lane, row by row
-        __syncwarp();
+      if (!tma) {  // pitches, widths or addresses that TMA cannot take: a column to a lane, row by row
+        boxes_free();
         lin_box_write(boxes, lane, v, true, 0);
+        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
         __syncwarp();
-        lin_finish_column(e, boxes, lane, row0, col);
+        lin_finish_column<FINE, FULL>(e, boxes, lane, row0, col + lane);
+        lin_finish_column<FINE, FULL>(e, boxes + kLinBox, lane, row0, col + 32 + lane);
+        __syncwarp();
         return;
       }
-      if (e.bias) {
-        const float bias = col + lane < e.n ? __ldg(e.bias + col + lane) : 0.f;
+      if (has_bias) {
+        const float b0 = col + lane < n ? __ldg(e.bias + col + lane) : 0.f;
+        const float b1 = col + 32 + lane < n ? __ldg(e.bias + col + 32 + lane) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, bias, i);
+        for (int i = 0; i < 32; ++i) {
+          v[i] += __shfl_sync(0xffffffffu, b0, i);
+          v[32 + i] += __shfl_sync(0xffffffffu, b1, i);
+        }
       }
-      if (e.z && row0 + lane < e.m) {  // two whole sectors of this lane's row
+      if (has_z && row0 + lane < m) {  // whole sectors of this lane's row
         __nv_bfloat16* zp = e.z + (row0 + lane) * e.z_ld + col;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          if (col + i < e.n)
+        for (int i = 0; i < 64; i += 8)
+          if (col + i < n)
             *reinterpret_cast<uint4*>(zp + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
                                                            pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
       }
-      if (e.act == kActSilu) {
+      if (act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActSilu);
-      } else if (e.act == kActGelu) {
+        for (int i = 0; i < 64; ++i) v[i] = lin_act(v[i], kActSilu);
+      } else if (act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActGelu);
+        for (int i = 0; i < 64; ++i) v[i] = lin_act(v[i], kActGelu);
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= e.alpha;
-      const int at = (32 * q) & (round_cols - 1);  // within the round
-      const bool first = at == 0;
+      for (int i = 0; i < 64; ++i) v[i] *= alpha;
+      const bool first = h == 0 || !wide;  // of a round
       if (load_res) {
         if (first) {
           if (!mbar_wait(rbar, res_phase, 0x307)) { ok = false; return; }
           res_phase ^= 1;
           res_due = false;
         }
-        // (64 columns of a bf16 residual lie in the box that the second 32 of an fp32 output take)
-        lin_box_add(boxes + (e.res_f32 ? at >> 5 : (e.out_f32 ? 1 : at >> 6)) * kLinBox, lane, v, e.res_f32,
-                    (at >> 5) & 1);
+        if (res32) {
+          lin_box_add(boxes, lane, v, true, 0);
+          lin_box_add(boxes + kLinBox, lane, v + 32, true, 0);
+        } else {
+          uint8_t* box = boxes + (FINE ? 1 : h) * kLinBox;
+          lin_box_add(box, lane, v, false, 0);
+          lin_box_add(box, lane, v + 32, false, 1);
+        }
       } else if (first) {
         boxes_free();
       }
-      lin_box_write(boxes + (e.out_f32 ? at >> 5 : at >> 6) * kLinBox, lane, v, e.out_f32, (at >> 5) & 1);
-      if (last || at + 32 == round_cols) {
-        store_round(e.out_f32 ? 32 : 64, at + 32, row0, col - at);
-        if (load_res && !last && lane == 0) fetch_res(row0, col + 32);
+      if (FINE) {
+        lin_box_write(boxes, lane, v, true, 0);
+        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
+      } else {
+        uint8_t* box = boxes + (wide ? h : 0) * kLinBox;
+        lin_box_write(box, lane, v, false, 0);
+        lin_box_write(box, lane, v + 32, false, 1);
+      }
+      if (!wide || last) {
+        store_boxes(wide ? 64 * (h + 1) : 64, row0, wide ? col0 : col);
+        if (load_res && !last && lane == 0) fetch_res(row0, col + 64);
       }
     };
     for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
       for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
         const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
         const int col0 = p.ni * 256 + part * 128;
-        int blocks = row0 < e.m && col0 < e.n ? (e.n - col0 + 31) / 32 : 0;  // of 32 columns
-        if (blocks > 4) blocks = 4;
-        if (load_res && p.slot < 0 && lane == 0 && blocks > 0) fetch_res(row0, col0);  // during the main loop
+        const int halves = row0 < m && col0 < n ? (col0 + 64 < n ? 2 : 1) : 0;  // of 64 columns, in the matrix
+        if (load_res && p.slot < 0 && lane == 0 && halves > 0) fetch_res(row0, col0);  // under the main loop
         if (FINE) {
           const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
           float acc[128];
@@ -579,14 +629,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             release(buf);
           }
 #pragma unroll 1
-          for (int q = 0; ok && q < blocks; ++q) {
-            float v[32];
+          for (int h = 0; ok && h < halves; ++h) {
+            float v[64];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float lo = q & 1 ? acc[32 + j] : acc[j], hi = q & 1 ? acc[96 + j] : acc[64 + j];
-              v[j] = q & 2 ? hi : lo;
-            }
-            finish(v, q, row0, col0, q == blocks - 1);
+            for (int j = 0; j < 64; ++j) v[j] = h ? acc[64 + j] : acc[j];
+            finish(v, h, row0, col0, h == halves - 1);
           }
         } else {
           const int buf = chunk & 1;
@@ -595,13 +642,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tc_fence_after();
           const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-          for (int q = 0; ok && q < blocks; ++q) {
-            float v[32];
-            tmem_ld32(taddr + 32 * q, v);
-            if (q == blocks - 1) release(buf);
-            finish(v, q, row0, col0, q == blocks - 1);
+          for (int h = 0; ok && h < halves; ++h) {
+            float v[64];
+            tmem_ld64(taddr + 64 * h, v);
+            if (h == halves - 1) release(buf);
+            finish(v, h, row0, col0, h == halves - 1);
           }
-          if (blocks == 0) release(buf);
+          if (halves == 0) release(buf);
         }
       }
     }
@@ -864,14 +911,14 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks) {
   return p;
 }
 
-template <bool AMN, bool BMN, bool FINE>
+template <bool AMN, bool BMN, bool FINE, bool FULL>
 static int launch_lin_one(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const CUtensorMap& mr,
                           const LinGemmArgs& g, cudaStream_t s) {
   static int pairs_dev[kMaxDevices] = {};
   const int dev = current_device();
   if (dev < 0) return -1;
   int& pairs = pairs_dev[dev];
-  auto kernel = linear_gemm_kernel<AMN, BMN, FINE>;
+  auto kernel = linear_gemm_kernel<AMN, BMN, FINE, FULL>;
   if (pairs == 0) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem) != cudaSuccess) return -1;
     cudaLaunchConfig_t cfg = {};
@@ -942,12 +989,22 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
                     (epi.res && make_map_rows32(&mr, epi.res, epi.n, epi.m, epi.res_ld, epi.res_f32))))
     return -2;
   int rc;
-  if (!a.mn_major && !b.mn_major)
-    rc = epi.out_f32 ? launch_lin_one<false, false, true>(ma, mb, mo, mr, g, s) : launch_lin_one<false, false, false>(ma, mb, mo, mr, g, s);
-  else if (!a.mn_major)
-    rc = epi.out_f32 ? launch_lin_one<false, true, true>(ma, mb, mo, mr, g, s) : launch_lin_one<false, true, false>(ma, mb, mo, mr, g, s);
-  else
-    rc = epi.out_f32 ? launch_lin_one<true, true, true>(ma, mb, mo, mr, g, s) : launch_lin_one<true, true, false>(ma, mb, mo, mr, g, s);
+  const bool fine = epi.out_f32, full = epi.bias || epi.z || epi.act != kActNone;
+  if (a.mn_major) {
+    if (full) return -2;
+    rc = fine ? launch_lin_one<true, true, true, false>(ma, mb, mo, mr, g, s)
+              : launch_lin_one<true, true, false, false>(ma, mb, mo, mr, g, s);
+  } else if (b.mn_major) {
+    if (full) return -2;
+    rc = fine ? launch_lin_one<false, true, true, false>(ma, mb, mo, mr, g, s)
+              : launch_lin_one<false, true, false, false>(ma, mb, mo, mr, g, s);
+  } else if (full) {
+    rc = fine ? launch_lin_one<false, false, true, true>(ma, mb, mo, mr, g, s)
+              : launch_lin_one<false, false, false, true>(ma, mb, mo, mr, g, s);
+  } else {
+    rc = fine ? launch_lin_one<false, false, true, false>(ma, mb, mo, mr, g, s)
+              : launch_lin_one<false, false, false, false>(ma, mb, mo, mr, g, s);
+  }
   if (rc || !plan.cut) return rc;
   const cudaError_t e =
       launch_kernel(linear_finish_kernel, dim3(plan.part_rb * plan.part_cb, plan.cut), dim3(256), 0, s, 1, g);
