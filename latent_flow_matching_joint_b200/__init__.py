@@ -474,59 +474,76 @@ def klein_op_time_mod(model: KleinModel, sigma: float, sigma_next: float, with_r
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 
 
+_torch = None  # torch once a training op has been called; nothing else here needs it at import
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _refuse(code: int, msg: str):
     raise KleinError(code, msg)
 
 
-def _same_device(device, tensors):
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            _refuse(-1, f"{name} is on {t.device}, not on {device}")
+def _device_of(first, tensors):
+    """Index of the CUDA device that all tensors (or None) are on."""
+    dev = first.get_device()
+    if dev < 0:
+        _refuse(-1, f"tensors on {first.device}: CUDA tensors needed")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(-1, f"a tensor is on {t.device}, not on {first.device}")
+    return dev
 
 
-def _run_on(device, call, stream):
-    """call(stream handle) with `device` current."""
-    import torch
-    if device.type != "cuda":
-        _refuse(-1, f"tensors on {device}: CUDA tensors needed")
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
-    else:
-        with torch.cuda.device(device):
-            _check(call(_stream(stream)))
+def _run_on(dev: int, stream, function, *args):
+    """function(*args, stream) with the device current, on its current stream unless one is given."""
+    torch = _torch
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _run_on(dev, stream, function, *args)
+    rc = function(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
+    if rc < 0:
+        _check(rc)
 
 
 def _heads(name, t, shape):
-    import torch
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _torch.bfloat16:
         _refuse(-1, f"{name} has type {t.dtype}, not bfloat16")
-    if tuple(t.shape) != shape:
-        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.shape != shape:
+        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     sb, sh, sr, sd = t.stride()
     if sd != 1:
         _refuse(-2, f"{name} is not contiguous along its last dimension")
-    return ctypes.byref(KleinHeads(t.data_ptr(), sb, sh, sr))
+    return KleinHeads(t.data_ptr(), sb, sh, sr)
 
 
 def _attention_shape(q, k, n_txt, txt_len, scale):
-    import torch
+    if _torch is None:
+        _load_torch()
     if q.dim() != 4 or k.dim() != 4:
         _refuse(-2, "q and k must be [batch, heads, rows, 128]")
-    batch, heads, rows, _ = q.shape
-    s = KleinAttentionShape(batch, heads, k.shape[1], rows, n_txt, None, HEAD_DIM ** -0.5 if scale is None else scale)
+    qs = q.shape
+    batch, heads, rows, d = qs
+    kv_heads = k.shape[1]
+    if d != HEAD_DIM:
+        _refuse(-2, f"q has heads of {d}, not {HEAD_DIM}")
     if txt_len is not None:
-        _vector("txt_len", txt_len, batch, torch.int32)
-        s.txt_len = txt_len.data_ptr()
-    return s, (batch, heads, rows, HEAD_DIM), (batch, k.shape[1], rows, HEAD_DIM)
+        _vector("txt_len", txt_len, batch, _torch.int32)
+        txt_len = txt_len.data_ptr()
+    s = KleinAttentionShape(batch, heads, kv_heads, rows, n_txt, txt_len, HEAD_DIM ** -0.5 if scale is None else scale)
+    return s, qs, qs if kv_heads == heads else _torch.Size((batch, kv_heads, rows, d))
 
 
 def _statistics(lse, shape):
-    import torch
-    if lse.dtype != torch.float32:
+    if lse.dtype != _torch.float32:
         _refuse(-1, f"lse has type {lse.dtype}, not float32")
-    if tuple(lse.shape) != shape or not lse.is_contiguous():
-        _refuse(-2, f"lse is not a contiguous {shape} tensor")
-    return _ptr(lse)
+    if lse.shape != shape or not lse.is_contiguous():
+        _refuse(-2, f"lse is not a contiguous {tuple(shape)} tensor")
+    return lse.data_ptr()
 
 
 def klein_op_attention_forward(q, k, v, out, lse, n_txt: int = 0, txt_len=None, scale: float | None = None,
@@ -538,10 +555,9 @@ def klein_op_attention_forward(q, k, v, out, lse, n_txt: int = 0, txt_len=None, 
     (int32 [batch] on the device) rows [txt_len, n_txt) of an item are padding.
     scale: 1/sqrt(128) unless given."""
     shape, qs, ks = _attention_shape(q, k, n_txt, txt_len, scale)
-    args = (_heads("q", q, qs), _heads("k", k, ks), _heads("v", v, ks), _heads("out", out, qs),
-            _statistics(lse, qs[:3]))
-    _same_device(q.device, (("k", k), ("v", v), ("out", out), ("lse", lse), ("txt_len", txt_len)))
-    _run_on(q.device, lambda s: lib.klein_op_attention_forward(ctypes.byref(shape), *args, s), stream)
+    dev = _device_of(q, (k, v, out, lse, txt_len))
+    _run_on(dev, stream, lib.klein_op_attention_forward, shape, _heads("q", q, qs), _heads("k", k, ks),
+            _heads("v", v, ks), _heads("out", out, qs), _statistics(lse, qs[:3]))
 
 
 def klein_attention_backward_workspace_size(batch: int, heads: int, rows: int, n_txt: int = 0) -> int:
@@ -555,33 +571,34 @@ def klein_op_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, ws, n_txt: 
     like k. ws: klein_attention_backward_workspace_size(batch, heads, rows, n_txt)
     bytes."""
     shape, qs, ks = _attention_shape(q, k, n_txt, txt_len, scale)
-    inputs = (_heads("q", q, qs), _heads("k", k, ks), _heads("v", v, ks), _heads("out", out, qs),
-              _statistics(lse, qs[:3]), _heads("dout", dout, qs))
-    outputs = (_heads("dq", dq, qs), _heads("dk", dk, ks), _heads("dv", dv, ks))
-    _same_device(q.device, (("k", k), ("v", v), ("out", out), ("lse", lse), ("dout", dout), ("dq", dq), ("dk", dk),
-                            ("dv", dv), ("ws", ws), ("txt_len", txt_len)))
+    dev = _device_of(q, (k, v, out, lse, dout, dq, dk, dv, ws, txt_len))
     ws_ptr, ws_bytes = _workspace(ws)
-    _run_on(q.device, lambda s: lib.klein_op_attention_backward(ctypes.byref(shape), *inputs, *outputs, ws_ptr,
-                                                                 ws_bytes, s), stream)
+    _run_on(dev, stream, lib.klein_op_attention_backward, shape, _heads("q", q, qs), _heads("k", k, ks),
+            _heads("v", v, ks), _heads("out", out, qs), _statistics(lse, qs[:3]), _heads("dout", dout, qs),
+            _heads("dq", dq, qs), _heads("dk", dk, ks), _heads("dv", dv, ks), ws_ptr, ws_bytes)
 
 
-def _matrix(name, t, shape, types):
-    """Row pitch of a 2-D tensor with unit column stride."""
-    if t.dtype not in types:
-        _refuse(-1, f"{name} has type {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+def _matrix(name, t, rows, cols, dtype=None):
+    """Address, row pitch and whether it is fp32 of a 2-D tensor with unit column stride."""
+    dt = t.dtype
+    f32 = dt == _torch.float32
+    if dt != dtype and (dtype is not None or not (f32 or dt == _torch.bfloat16)):
+        _refuse(-1, f"{name} has type {dt}")
+    if t.shape != (rows, cols):
+        _refuse(-2, f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         _refuse(-2, f"{name} is not contiguous along its last dimension")
-    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8  # the pitch of a single row is never used
+    # the pitch of a single row is never used
+    return t.data_ptr(), ld if rows > 1 else (cols + 7) // 8 * 8, f32
 
 
 def _vector(name, t, n, dtype):
     if t.dtype != dtype:
         _refuse(-1, f"{name} has type {t.dtype}, not {dtype}")
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         _refuse(-2, f"{name} is not a contiguous vector of {n}")
+    return t.data_ptr()
 
 
 def _workspace(ws):
@@ -589,13 +606,18 @@ def _workspace(ws):
         return None, 0
     if not ws.is_contiguous():
         _refuse(-2, "the workspace is not contiguous")
-    return _ptr(ws), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
-def _activation(act):
+def _linear_sizes(x, w, act):
+    if _torch is None:
+        _load_torch()
+    if x.dim() != 2 or w.dim() != 2:
+        _refuse(-2, "x and w must be matrices")
     if act not in ACTIVATIONS:
         _refuse(-1, f"unknown activation {act!r}")
-    return ACTIVATIONS[act]
+    m, k = x.shape
+    return m, w.shape[0], k, ACTIVATIONS[act]
 
 
 def klein_linear_workspace_size(m: int, n: int, k: int) -> int:
@@ -608,29 +630,18 @@ def klein_op_linear(x, w, out, ws=None, bias=None, residual=None, act: str = "no
     float32 [n], residual and out bf16 or float32 [m, n] (residual may be out),
     preact bf16 [m, n] receives x w^T + bias. act: "none", "silu", "gelu" (tanh
     form). ws: klein_linear_workspace_size(m, n, k) bytes."""
-    import torch
-    bf16, both = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    if x.dim() != 2 or w.dim() != 2:
-        _refuse(-2, "x and w must be matrices")
-    (m, k), n = x.shape, w.shape[0]
-    a = KleinLinearArgs()
-    a.m, a.n, a.k = m, n, k
-    a.x, a.x_ld = x.data_ptr(), _matrix("x", x, (m, k), bf16)
-    a.w, a.w_ld = w.data_ptr(), _matrix("w", w, (n, k), bf16)
-    a.out, a.out_ld, a.out_f32 = out.data_ptr(), _matrix("out", out, (m, n), both), out.dtype == torch.float32
-    if bias is not None:
-        _vector("bias", bias, n, torch.float32)
-        a.bias = bias.data_ptr()
-    if residual is not None:
-        a.residual, a.residual_ld = residual.data_ptr(), _matrix("residual", residual, (m, n), both)
-        a.residual_f32 = residual.dtype == torch.float32
-    if preact is not None:
-        a.preact, a.preact_ld = preact.data_ptr(), _matrix("preact", preact, (m, n), bf16)
-    a.act, a.alpha = _activation(act), alpha
-    _same_device(x.device, (("w", w), ("out", out), ("ws", ws), ("bias", bias), ("residual", residual),
-                            ("preact", preact)))
+    m, n, k, act_code = _linear_sizes(x, w, act)
+    bf16 = _torch.bfloat16
+    dev = _device_of(x, (w, out, ws, bias, residual, preact))
+    xp, x_ld, _ = _matrix("x", x, m, k, bf16)
+    wp, w_ld, _ = _matrix("w", w, n, k, bf16)
+    op, o_ld, o_f32 = _matrix("out", out, m, n)
+    rp, r_ld, r_f32 = (None, 0, 0) if residual is None else _matrix("residual", residual, m, n)
+    zp, z_ld, _ = (None, 0, 0) if preact is None else _matrix("preact", preact, m, n, bf16)
+    bp = None if bias is None else _vector("bias", bias, n, _torch.float32)
+    a = KleinLinearArgs(m, n, k, xp, x_ld, wp, w_ld, bp, rp, r_ld, r_f32, act_code, alpha, op, o_ld, o_f32, zp, z_ld)
     ws_ptr, ws_bytes = _workspace(ws)
-    _run_on(x.device, lambda s: lib.klein_op_linear(ctypes.byref(a), ws_ptr, ws_bytes, s), stream)
+    _run_on(dev, stream, lib.klein_op_linear, a, ws_ptr, ws_bytes)
 
 
 def klein_linear_backward_workspace_size(m: int, n: int, k: int) -> int:
@@ -643,28 +654,17 @@ def klein_op_linear_backward(dout, x, w, ws, dx=None, dw=None, dbias=None, preac
     dw = dz^T x, dbias = dz summed over rows, each written if given. dout, dx and
     dw bf16 or float32, dbias float32. ws: klein_linear_backward_workspace_size
     (m, n, k) bytes."""
-    import torch
-    bf16, both = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    if x.dim() != 2 or w.dim() != 2:
-        _refuse(-2, "x and w must be matrices")
-    (m, k), n = x.shape, w.shape[0]
-    a = KleinLinearGradArgs()
-    a.m, a.n, a.k = m, n, k
-    a.dout, a.dout_ld = dout.data_ptr(), _matrix("dout", dout, (m, n), both)
-    a.dout_f32 = dout.dtype == torch.float32
-    a.x, a.x_ld = x.data_ptr(), _matrix("x", x, (m, k), bf16)
-    a.w, a.w_ld = w.data_ptr(), _matrix("w", w, (n, k), bf16)
-    if preact is not None:
-        a.preact, a.preact_ld = preact.data_ptr(), _matrix("preact", preact, (m, n), bf16)
-    if dx is not None:
-        a.dx, a.dx_ld, a.dx_f32 = dx.data_ptr(), _matrix("dx", dx, (m, k), both), dx.dtype == torch.float32
-    if dw is not None:
-        a.dw, a.dw_ld, a.dw_f32 = dw.data_ptr(), _matrix("dw", dw, (n, k), both), dw.dtype == torch.float32
-    if dbias is not None:
-        _vector("dbias", dbias, n, torch.float32)
-        a.dbias = dbias.data_ptr()
-    a.act, a.alpha = _activation(act), alpha
-    _same_device(x.device, (("dout", dout), ("w", w), ("ws", ws), ("preact", preact), ("dx", dx), ("dw", dw),
-                            ("dbias", dbias)))
+    m, n, k, act_code = _linear_sizes(x, w, act)
+    bf16 = _torch.bfloat16
+    dev = _device_of(dout, (x, w, ws, dx, dw, dbias, preact))
+    gp, g_ld, g_f32 = _matrix("dout", dout, m, n)
+    xp, x_ld, _ = _matrix("x", x, m, k, bf16)
+    wp, w_ld, _ = _matrix("w", w, n, k, bf16)
+    zp, z_ld, _ = (None, 0, 0) if preact is None else _matrix("preact", preact, m, n, bf16)
+    dxp, dx_ld, dx_f32 = (None, 0, 0) if dx is None else _matrix("dx", dx, m, k)
+    dwp, dw_ld, dw_f32 = (None, 0, 0) if dw is None else _matrix("dw", dw, n, k)
+    dbp = None if dbias is None else _vector("dbias", dbias, n, _torch.float32)
+    a = KleinLinearGradArgs(m, n, k, gp, g_ld, g_f32, xp, x_ld, wp, w_ld, zp, z_ld, act_code, alpha, dxp, dx_ld, dx_f32,
+                            dwp, dw_ld, dw_f32, dbp)
     ws_ptr, ws_bytes = _workspace(ws)
-    _run_on(x.device, lambda s: lib.klein_op_linear_backward(ctypes.byref(a), ws_ptr, ws_bytes, s), stream)
+    _run_on(dev, stream, lib.klein_op_linear_backward, a, ws_ptr, ws_bytes)

@@ -200,8 +200,8 @@ LinPlan plan_linear(long long m, long long n, long long k_blocks);
 // together with B; bias, z and activation only with both k-contiguous. Returns 0, -1 (launch) or -2 (tensor map).
 int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const LinEpi& epi, float* partial,
                        cudaStream_t stream);
-// The same for at most 4 rows of k-contiguous operands, without tensor cores.
-constexpr int kLinMaxRows = 4;
+// The same for few rows of k-contiguous operands, the weights read straight into registers.
+bool linear_rows_fit(int m, int n, int k);
 int launch_linear_rows(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                        const LinEpi& epi, cudaStream_t stream);
 

@@ -1310,7 +1310,7 @@ static int check_matrix(const char* name, const void* p, long long ld, int cols,
 }
 
 size_t klein_linear_workspace_size(int m, int n, int k) {
-  if (m < 1 || n < 1 || k < 1 || m <= kLinMaxRows) return 0;
+  if (m < 1 || n < 1 || k < 1 || linear_rows_fit(m, n, k)) return 0;
   return plan_linear(m, n, ((long long)k + 63) / 64).partial_bytes;
 }
 
@@ -1347,7 +1347,7 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
   e.alpha = a->alpha;
   e.act = a->act;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->m <= kLinMaxRows)
+  if (linear_rows_fit(a->m, a->n, a->k))
     rc = launch_linear_rows(static_cast<const __nv_bfloat16*>(a->x), a->x_ld, static_cast<const __nv_bfloat16*>(a->w),
                             a->w_ld, a->k, e, s);
   else

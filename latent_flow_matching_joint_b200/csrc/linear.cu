@@ -697,85 +697,122 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinGemmArgs g)
   lin_finish4(g.epi, row, col, v, lin_bias4(g.epi, col));
 }
 
-// Few rows (m <= MV <= 4): the weights are read once, straight into registers,
-// WPO warps per output column (8 when there are too few columns to fill the
-// GPU with one warp each), fp32 FMAs, one value per row and warp reduced by
-// shuffles. Bound by the weights' bytes.
-template <int MV, int WPO>
-__global__ void __launch_bounds__(256) linear_rows_kernel(const __nv_bfloat16* x, long long x_ld,
+// Eight bf16 of a row from column k on, zeros past the row's end.
+__device__ __forceinline__ uint4 lin_load8(const __nv_bfloat16* row, int k, int k_end) {
+  if (k + 8 <= k_end) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t u[4] = {0u, 0u, 0u, 0u};
+  const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (k + i < k_end) u[i >> 1] |= static_cast<uint32_t>(__ldg(r + k + i)) << (16 * (i & 1));
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ void lin_mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Few rows (m <= 8 NB): the weights' bytes are all that counts, and they go
+// straight from memory into registers. A block takes 16 columns (rows of w),
+// its WARPS warps every WARPS-th stretch of 128 of k (16 warps for long rows of
+// which there are too few to fill the SMs, else 8). Per 32 of k a lane loads 16
+// bytes of two weight rows and of one row of x per NB: with lane = 4 g + t,
+// row g (and g + 8) and k = 8 t .. 8 t + 7. Which elements of k a product step
+// pairs is free as long as both operands agree, so those registers are the
+// operands of two 16 x 8 x 16 warp-level products as they are, with weights as
+// A and rows of x as B. (The 5th generation's products want both operands
+// in shared memory and 128 rows; here the arithmetic is 1 % of the time.) The
+// warps' sums are added in shared memory in a fixed order; like the large
+// products they are moved to fp32 registers every 512 of k.
+template <int NB, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const __nv_bfloat16* x, long long x_ld,
                                                           const __nv_bfloat16* w, long long w_ld, int k,
                                                           const LinEpi e) {
-  __shared__ float part[8][MV];
+  __shared__ float part[WARPS][8 * NB][17];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * (8 / WPO) + warp / WPO;
-  float s[MV];
+  const int g = lane >> 2, t = lane & 3;
+  const int col0 = blockIdx.x * 16;
+  // (rows past the last are read again, and not stored)
+  const __nv_bfloat16* w0 = w + static_cast<long long>(col0 + g < e.n ? col0 + g : e.n - 1) * w_ld;
+  const __nv_bfloat16* w1 = w + static_cast<long long>(col0 + g + 8 < e.n ? col0 + g + 8 : e.n - 1) * w_ld;
+  const __nv_bfloat16* xr[NB];
 #pragma unroll
-  for (int m = 0; m < MV; ++m) s[m] = 0.f;
-  if (col < e.n) {
-    const __nv_bfloat16* wr = w + static_cast<long long>(col) * w_ld;
-    const int k8 = k & ~7;
-    auto add8 = [&](uint4 wv, int at) {
-      const float2 w0 = unpack_bf16(wv.x), w1 = unpack_bf16(wv.y), w2 = unpack_bf16(wv.z), w3 = unpack_bf16(wv.w);
+  for (int b = 0; b < NB; ++b) xr[b] = x + static_cast<long long>(8 * b + g < e.m ? 8 * b + g : e.m - 1) * x_ld;
+  float sum[NB][4], c[NB][4];
 #pragma unroll
-      for (int m = 0; m < MV; ++m) {
-        if (m < e.m) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(x + m * x_ld + at);
-          const float2 x0 = unpack_bf16(xv.x), x1 = unpack_bf16(xv.y), x2 = unpack_bf16(xv.z), x3 = unpack_bf16(xv.w);
-          s[m] = fmaf(w0.x, x0.x, fmaf(w0.y, x0.y, s[m]));
-          s[m] = fmaf(w1.x, x1.x, fmaf(w1.y, x1.y, s[m]));
-          s[m] = fmaf(w2.x, x2.x, fmaf(w2.y, x2.y, s[m]));
-          s[m] = fmaf(w3.x, x3.x, fmaf(w3.y, x3.y, s[m]));
-        }
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[b][i] = c[b][i] = 0.f;
+  auto step = [&](uint4 a, uint4 a8, const uint4* xv) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      lin_mma16816(c[b], a.x, a8.x, a.y, a8.y, xv[b].x, xv[b].y);
+      lin_mma16816(c[b], a.z, a8.z, a.w, a8.w, xv[b].z, xv[b].w);
+    }
+  };
+  int since = 0;
+  for (int k0 = warp * 128; k0 < k; k0 += 128 * WARPS) {
+    if (k0 + 128 <= k) {
+      uint4 a[4], a8[4], xv[4][NB];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = k0 + 32 * u + 8 * t;
+        a[u] = __ldg(reinterpret_cast<const uint4*>(w0 + at));
+        a8[u] = __ldg(reinterpret_cast<const uint4*>(w1 + at));
       }
-    };
-    constexpr int kStep = WPO * 256;
-    int at = (warp % WPO) * 256 + lane * 8;
-    for (; at + 3 * kStep < k8; at += 4 * kStep) {
-      uint4 wv[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) wv[u] = __ldg(reinterpret_cast<const uint4*>(wr + at + u * kStep));
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add8(wv[u], at + u * kStep);
+        for (int b = 0; b < NB; ++b) xv[u][b] = __ldg(reinterpret_cast<const uint4*>(xr[b] + k0 + 32 * u + 8 * t));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) step(a[u], a8[u], xv[u]);
+    } else {
+      for (int at = k0 + 8 * t; at - 8 * t < k; at += 32) {
+        uint4 xv[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) xv[b] = lin_load8(xr[b], at, k);
+        step(lin_load8(w0, at, k), lin_load8(w1, at, k), xv);
+      }
     }
-    for (; at < k8; at += kStep) add8(__ldg(reinterpret_cast<const uint4*>(wr + at)), at);
-    if (warp % WPO == 0 && k8 + lane < k) {  // the last k % 8 elements
-      const float wv = __bfloat162float(wr[k8 + lane]);
+    if (++since == 4) {
+      since = 0;
 #pragma unroll
-      for (int m = 0; m < MV; ++m)
-        if (m < e.m) s[m] = fmaf(wv, __bfloat162float(x[m * x_ld + k8 + lane]), s[m]);
-    }
-  }
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-  for (int m = 0; m < MV; ++m) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[m] += __shfl_xor_sync(0xffffffffu, s[m], o);
-  }
-  if (WPO > 1) {
-    if (lane == 0) {
-#pragma unroll
-      for (int m = 0; m < MV; ++m) part[warp][m] = s[m];
-    }
-    __syncthreads();
-    if (warp != 0) return;
-#pragma unroll
-    for (int m = 0; m < MV; ++m) {
-      s[m] = part[0][m];
-#pragma unroll
-      for (int i = 1; i < WPO; ++i) s[m] += part[i][m];
+        for (int i = 0; i < 4; ++i) {
+          sum[b][i] += c[b][i];
+          c[b][i] = 0.f;
+        }
     }
   }
-  float v = s[0];
+  // element (column g or g + 8 of w's 16, row 2 t or 2 t + 1 of x's 8)
 #pragma unroll
-  for (int m = 1; m < MV; ++m) v = lane == m ? s[m] : v;
-  if (col < e.n && lane < MV && lane < e.m) {
+  for (int b = 0; b < NB; ++b) {
+    part[warp][8 * b + 2 * t][g] = sum[b][0] + c[b][0];
+    part[warp][8 * b + 2 * t + 1][g] = sum[b][1] + c[b][1];
+    part[warp][8 * b + 2 * t][g + 8] = sum[b][2] + c[b][2];
+    part[warp][8 * b + 2 * t + 1][g + 8] = sum[b][3] + c[b][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 128 * NB; i += 32 * WARPS) {
+    const int row = i >> 4, col = col0 + (i & 15);
+    if (row >= e.m || col >= e.n) continue;
+    float v = part[0][row][i & 15];
+#pragma unroll
+    for (int q = 1; q < WARPS; ++q) v += part[q][row][i & 15];
     const float z = v + (e.bias ? __ldg(e.bias + col) : 0.f);
-    const float r = e.res ? lin_load(e.res, lane * e.res_ld + col, e.res_f32) : 0.f;
-    if (e.z) e.z[lane * e.z_ld + col] = __float2bfloat16_rn(z);
+    const float r = e.res ? lin_load(e.res, row * e.res_ld + col, e.res_f32) : 0.f;
+    if (e.z) e.z[row * e.z_ld + col] = __float2bfloat16_rn(z);
     const float y = fmaf(e.alpha, lin_act(z, e.act), r);
-    if (e.out_f32) reinterpret_cast<float*>(e.out)[lane * e.out_ld + col] = y;
-    else reinterpret_cast<__nv_bfloat16*>(e.out)[lane * e.out_ld + col] = __float2bfloat16_rn(y);
+    if (e.out_f32) static_cast<float*>(e.out)[row * e.out_ld + col] = y;
+    else static_cast<__nv_bfloat16*>(e.out)[row * e.out_ld + col] = __float2bfloat16_rn(y);
   }
 }
 
@@ -1012,20 +1049,25 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
 
-template <int MV>
-static cudaError_t launch_rows_mv(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
+template <int NB>
+static cudaError_t launch_rows_nb(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                                   const LinEpi& e, cudaStream_t s) {
-  if (e.n < 8 * kLinSms && k >= 2048)  // one warp per column would leave most SMs with a few long serial rows
-    return launch_kernel(linear_rows_kernel<MV, 8>, dim3(e.n), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
-  return launch_kernel(linear_rows_kernel<MV, 1>, dim3((e.n + 7) / 8), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
+  const int blocks = (e.n + 15) / 16;
+  if (blocks < 4 * kLinSms && k >= 2048)
+    return launch_kernel(linear_rows_kernel<NB, 16>, dim3(blocks), dim3(512), 0, s, 1, x, x_ld, w, w_ld, k, e);
+  return launch_kernel(linear_rows_kernel<NB, 8>, dim3(blocks), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
 }
+
+// 16 rows or fewer, or up to 32 against a small matrix. Measured on one B200 (us, against the large product's
+// kernels): 8 x 27648 x 3072 29 (floor 26) against 50; 16 rows of it 33 against 38, 32 rows 54 against 39;
+// 32 x 640 x 640 2.9 against 7.
+bool linear_rows_fit(int m, int n, int k) { return m <= 16 || (m <= 32 && static_cast<long long>(n) * k <= (1 << 22)); }
 
 int launch_linear_rows(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                        const LinEpi& e, cudaStream_t s) {
-  cudaError_t rc;
-  if (e.m == 1) rc = launch_rows_mv<1>(x, x_ld, w, w_ld, k, e, s);
-  else if (e.m == 2) rc = launch_rows_mv<2>(x, x_ld, w, w_ld, k, e, s);
-  else rc = launch_rows_mv<4>(x, x_ld, w, w_ld, k, e, s);
+  const cudaError_t rc = e.m <= 8    ? launch_rows_nb<1>(x, x_ld, w, w_ld, k, e, s)
+                         : e.m <= 16 ? launch_rows_nb<2>(x, x_ld, w, w_ld, k, e, s)
+                                     : launch_rows_nb<4>(x, x_ld, w, w_ld, k, e, s);
   note_launch();
   return (rc == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
 }
