@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   LinPiece p;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (FINE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (FINE) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;
     const int part = (warp - 4) >> 2;  // which half of the tile's columns
     const LinEpi& e = g.epi;
@@ -717,8 +717,9 @@ __device__ __forceinline__ void lin_mma16816(float* c, uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Few rows (m <= 8 NB): the weights' bytes are all that counts, and they go
-// straight from memory into registers. A block takes 16 columns (rows of w),
+// Few rows, or little of everything: the weights' bytes are all that counts,
+// and they go straight from memory into registers. A block takes 8 NB rows of
+// x and 16 columns (rows of w),
 // its WARPS warps every WARPS-th stretch of 128 of k (16 warps for long rows of
 // which there are too few to fill the SMs, else 8). Per 32 of k a lane loads 16
 // bytes of two weight rows and of one row of x per NB: with lane = 4 g + t,
@@ -739,12 +740,13 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const __nv_bflo
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int col0 = blockIdx.x * 16;
+  const int row0 = blockIdx.y * 8 * NB, rows = e.m - row0;
   // (rows past the last are read again, and not stored)
   const __nv_bfloat16* w0 = w + static_cast<long long>(col0 + g < e.n ? col0 + g : e.n - 1) * w_ld;
   const __nv_bfloat16* w1 = w + static_cast<long long>(col0 + g + 8 < e.n ? col0 + g + 8 : e.n - 1) * w_ld;
   const __nv_bfloat16* xr[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) xr[b] = x + static_cast<long long>(8 * b + g < e.m ? 8 * b + g : e.m - 1) * x_ld;
+  for (int b = 0; b < NB; ++b) xr[b] = x + static_cast<long long>(row0 + (8 * b + g < rows ? 8 * b + g : rows - 1)) * x_ld;
   float sum[NB][4], c[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -802,15 +804,16 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const __nv_bflo
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 128 * NB; i += 32 * WARPS) {
-    const int row = i >> 4, col = col0 + (i & 15);
-    if (row >= e.m || col >= e.n) continue;
-    float v = part[0][row][i & 15];
+    const int r = i >> 4, col = col0 + (i & 15);
+    if (r >= rows || col >= e.n) continue;
+    float v = part[0][r][i & 15];
 #pragma unroll
-    for (int q = 1; q < WARPS; ++q) v += part[q][row][i & 15];
+    for (int q = 1; q < WARPS; ++q) v += part[q][r][i & 15];
+    const long long row = row0 + r;
     const float z = v + (e.bias ? __ldg(e.bias + col) : 0.f);
-    const float r = e.res ? lin_load(e.res, row * e.res_ld + col, e.res_f32) : 0.f;
+    const float res = e.res ? lin_load(e.res, row * e.res_ld + col, e.res_f32) : 0.f;
     if (e.z) e.z[row * e.z_ld + col] = __float2bfloat16_rn(z);
-    const float y = fmaf(e.alpha, lin_act(z, e.act), r);
+    const float y = fmaf(e.alpha, lin_act(z, e.act), res);
     if (e.out_f32) static_cast<float*>(e.out)[row * e.out_ld + col] = y;
     else static_cast<__nv_bfloat16*>(e.out)[row * e.out_ld + col] = __float2bfloat16_rn(y);
   }
@@ -1052,16 +1055,22 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
 template <int NB>
 static cudaError_t launch_rows_nb(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                                   const LinEpi& e, cudaStream_t s) {
-  const int blocks = (e.n + 15) / 16;
-  if (blocks < 4 * kLinSms && k >= 2048)
-    return launch_kernel(linear_rows_kernel<NB, 16>, dim3(blocks), dim3(512), 0, s, 1, x, x_ld, w, w_ld, k, e);
-  return launch_kernel(linear_rows_kernel<NB, 8>, dim3(blocks), dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
+  const dim3 grid((e.n + 15) / 16, (e.m + 8 * NB - 1) / (8 * NB));
+  if (grid.x * grid.y < 4 * kLinSms && k >= 2048)
+    return launch_kernel(linear_rows_kernel<NB, 16>, grid, dim3(512), 0, s, 1, x, x_ld, w, w_ld, k, e);
+  return launch_kernel(linear_rows_kernel<NB, 8>, grid, dim3(256), 0, s, 1, x, x_ld, w, w_ld, k, e);
 }
 
-// 16 rows or fewer, or up to 32 against a small matrix. Measured on one B200 (us, against the large product's
-// kernels): 8 x 27648 x 3072 29 (floor 26) against 50; 16 rows of it 33 against 38, 32 rows 54 against 39;
-// 32 x 640 x 640 2.9 against 7.
-bool linear_rows_fit(int m, int n, int k) { return m <= 16 || (m <= 32 && static_cast<long long>(n) * k <= (1 << 22)); }
+// 16 rows or fewer, or a small problem: blocks of 32 rows x 16 columns for about one round over the SMs, and not
+// much re-reading of the weights. Measured on one B200 (us, back to back, against linear_gemm_kernel): 8 x 27648 x 3072
+// 29 (floor 26) against 50; 16 rows of it 33 against 38, 32 rows 54 against 39; 96 x 640 x 640 3.3 against 7.5;
+// 96 x 3072 x 1024 7.5 against 11, 96 x 3072 x 3072 19 against 13; 256 x 1024 x 256 5.1 against 6.3, 512 rows of it
+// 9.2 against 6.3; 4608 x 16 x 3072 5.6 against 13.
+bool linear_rows_fit(int m, int n, int k) {
+  if (m <= 16) return true;
+  const long long row_blocks = (m + 31) / 32;
+  return row_blocks * ((n + 15) / 16) <= 640 && row_blocks * n * k <= 12ll << 20;
+}
 
 int launch_linear_rows(const __nv_bfloat16* x, long long x_ld, const __nv_bfloat16* w, long long w_ld, int k,
                        const LinEpi& e, cudaStream_t s) {
