@@ -89,7 +89,10 @@ def check_forward(kb, m, n, k, act="none", bias=False, residual=None, out=torch.
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 256, 256), (1, 17, 2500), (2, 1000, 77), (3, 9, 4096), (4, 2049, 320),
                                    (5, 128, 64), (5, 1, 9), (16, 16, 16), (80, 24, 1000), (127, 129, 65), (128, 128, 4096),
                                    (129, 255, 513), (300, 100, 5000), (512, 1280, 2560), (1961, 37, 130),
-                                   (1961, 2049, 200), (2560, 5120, 1088), (4608, 16, 2560), (4608, 9216, 16)])
+                                   (1961, 2049, 200), (2560, 5120, 1088), (4608, 16, 2560), (4608, 9216, 16),
+                                   (16, 16, 12289), (17, 3000, 5000), (33, 40, 12300), (97, 2000, 515), (640, 544, 64),
+                                   (700, 300, 5000), (1000, 515, 1027), (300, 1104, 2048), (5000, 24, 4104),
+                                   (257, 257, 5003)])
 def test_linear_shapes(kb, m, n, k):
     check_forward(kb, m, n, k)
     check_forward(kb, m, n, k, act="gelu", bias=True, residual=torch.float32, out=torch.float32, save=True, alpha=0.5,
@@ -100,16 +103,16 @@ def test_linear_shapes(kb, m, n, k):
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 @pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("m", [3, 200])
-def test_linear_epilogues(kb, act, residual, out, m):
-    check_forward(kb, m, 136, 200, act=act, bias=True, residual=residual, out=out, save=True, alpha=2.0)
-    check_forward(kb, m, 131, 200, act=act, residual=residual, out=out, alpha=-1.0, pad=1)
+@pytest.mark.parametrize("m,k", [(3, 200), (200, 200), (1500, 2056)])  # the last on the large product's kernel
+def test_linear_epilogues(kb, act, residual, out, m, k):
+    check_forward(kb, m, 136, k, act=act, bias=True, residual=residual, out=out, save=True, alpha=2.0)
+    check_forward(kb, m, 131, k, act=act, residual=residual, out=out, alpha=-1.0, pad=1)
     if residual is out:
-        check_forward(kb, m, 136, 200, act=act, residual=residual, out=out, in_place=True)
+        check_forward(kb, m, 136, k, act=act, residual=residual, out=out, in_place=True)
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m,n,k", [(2, 100, 3000), (64, 100, 12288), (300, 700, 9216)])
+@pytest.mark.parametrize("m,n,k", [(2, 100, 3000), (64, 100, 12288), (300, 700, 9216), (2000, 3000, 4096)])
 def test_linear_long_sums_keep_fp32(kb, m, n, k):
     """fp32 output of long sums: the norm of the error is that of fp32 sums, not of a truncating accumulator
     (1.1e-9 k = 1e-5 at k = 9216)."""
@@ -236,7 +239,7 @@ def test_linear_gradients_match_differences(kb):
 
 @pytest.mark.gpu
 def test_linear_same_bits_every_time(kb):
-    m, n, k = 100, 70, 9000  # split over k
+    m, n, k = 200, 300, 9000  # split over k
     x, w, dout = randn(1, m, k).bfloat16(), randn(2, n, k).bfloat16(), randn(3, m, n).bfloat16()
     assert kb.klein_linear_workspace_size(m, n, k) > 0
     first = None
@@ -255,7 +258,7 @@ def test_linear_same_bits_every_time(kb):
 
 @pytest.mark.gpu
 def test_linear_on_a_stream_and_in_a_graph(kb):
-    m, n, k = 200, 300, 4096
+    m, n, k = 200, 300, 12288
     x, w, r = randn(1, m, k).bfloat16(), randn(2, n, k).bfloat16(), randn(3, m, n)
     ws = torch.empty(kb.klein_linear_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
     want = torch.empty(m, n, device="cuda")
