@@ -41,6 +41,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kFwdBar = 6 * kAtTile;     // 2 query tiles, 2 stages of K, 2 of V
 constexpr int kFwdSmem = kFwdBar + 256 + 1024;
 
+#ifndef KLEIN_BWD_WARPS
+#define KLEIN_BWD_WARPS 16
+#endif
+constexpr int kBwdWarps = KLEIN_BWD_WARPS;         // elementwise warps of the backward kernel
+constexpr int kBwdThreads = 64 + 32 * kBwdWarps;
+constexpr int kBwdCols = 128 / (kBwdWarps / 4);    // columns of a tile per warp
 constexpr int kBwdStat = 6 * kAtTile;    // 2 resident tiles, 2 stages of 2 streamed tiles, then 2 stages of statistics
 constexpr int kStatBytes = 2 * 128 * 4;
 constexpr int kBwdBar = kBwdStat + 2 * kStatBytes;
@@ -145,6 +151,29 @@ __device__ __forceinline__ void mma_across_half(uint32_t d_tmem, uint32_t a_tmem
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
     umma_bf16_tmem_a(d_tmem, a_tmem + kk * 8, across_desc(b0 + kk * 2048), kIdescAcross, accumulate || kk != 0);
+}
+
+// The whole contraction, A as the backward kernel's warps leave it: each
+// kBwdCols columns' packed values at the start of those columns.
+__device__ __forceinline__ void mma_across_bwd(uint32_t d_tmem, uint32_t a_tmem, const uint8_t* b, bool accumulate) {
+  const uint32_t b0 = smem_u32(b);
+  constexpr int kSteps = kBwdCols / 16;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_bf16_tmem_a(d_tmem, a_tmem + (kk / kSteps) * kBwdCols + (kk % kSteps) * 8, across_desc(b0 + kk * 2048),
+                     kIdescAcross, accumulate || kk != 0);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* v) {
+  if (N == 64) tmem_ld64(taddr, v);
+  else tmem_ld32(taddr, v);
+}
+
+template <int N>  // N packed columns
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* v) {
+  if (N == 32) tmem_st32(taddr, reinterpret_cast<const float*>(v));
+  else tmem_st16(taddr, v);
 }
 
 __device__ __forceinline__ __nv_bfloat16* head_row(const HeadsView& v, int b, int head, int row) {
@@ -468,7 +497,7 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
 // while they make dS_j it runs dV_j and S_{j+1}.
 // dQ block: lanes are queries, columns keys. S = Q K^T (two buffers), dP = dO V^T,
 // dQ += dS K.
-__global__ void __launch_bounds__(kAtThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attn_train_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                           const AttnTrainArgs a) {
@@ -513,8 +542,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_init(&s_full[s], 1);
     }
     mbar_init(dp_full, 1);
-    mbar_init(p_ready, 256);
-    mbar_init(ds_ready, 256);
+    mbar_init(p_ready, kBwdWarps);
+    mbar_init(ds_ready, kBwdWarps);
     mbar_init(done, 1);
     mbar_init(scrub, 1);
     fence_barrier_init();
@@ -621,8 +650,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           const int st = j & 1, nx = (j + 1) & 1;
           if (!mbar_wait(p_ready, j & 1, 0x414)) break;
           tc_fence_after();
-          mma_across_half(t_dv, t_s, sm_t + st * kAtTile, 0, j > 0);
-          mma_across_half(t_dv, t_s + 64, sm_t + st * kAtTile, 1, true);
+          mma_across_bwd(t_dv, t_s, sm_t + st * kAtTile, j > 0);
           if (j + 1 < n) {
             if (!wait_in(s_in, j + 1)) break;
             mma_along(t_s, sm_x, sm_s + nx * kAtTile);
@@ -630,8 +658,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           if (!mbar_wait(ds_ready, j & 1, 0x415)) break;
           tc_fence_after();
-          mma_across_half(t_dk, t_dp, sm_s + st * kAtTile, 0, j > 0);
-          mma_across_half(t_dk, t_dp + 64, sm_s + st * kAtTile, 1, true);
+          mma_across_bwd(t_dk, t_dp, sm_s + st * kAtTile, j > 0);
           umma_commit(&st_empty[st]);
           if (j + 1 < n) {
             if (!wait_in(t_in, j + 1)) break;
@@ -660,8 +687,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           }
           if (!mbar_wait(ds_ready, j & 1, 0x416)) break;
           tc_fence_after();
-          mma_across_half(t_dq, t_dp, sm_s + st * kAtTile, 0, j > 0);
-          mma_across_half(t_dq, t_dp + 64, sm_s + st * kAtTile, 1, true);
+          mma_across_bwd(t_dq, t_dp, sm_s + st * kAtTile, j > 0);
           umma_commit(&st_empty[st]);
           if (j + 1 < n) {
             if (!wait_in(t_in, j + 1)) break;
@@ -675,25 +701,31 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       mbar_wait(done, 0, 0x41a);
     }
   } else {
+    constexpr int kC = kBwdCols;
     const int quarter = warp & 3;
-    const int part = (warp - 2) >> 2;  // half of the columns
+    const int part = (warp - 2) >> 2;  // which kC of the columns
     const int rloc = quarter * 32 + lane;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + part * kC;
     const float sl2 = a.scale_log2;
     bool ok = true;
-    float p[64], d[64];
+    float p[kC], d[kC];
+    uint32_t pk[kC / 2];
+    auto hand_over = [&](uint32_t col, uint64_t* bar) {  // the packed values, to the MMA warp
+      tmem_st_cols<kC / 2>(col, pk);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     if (is_kv) {
-      const uint32_t s_col = lane_base + part * 64, dp_col = lane_base + 128 + part * 64;
       for (int j = 0; j < n; ++j) {
         // the statistics came with the first streamed tile, which S^T has been made from
-        const float4* lse = reinterpret_cast<const float4*>(sm_stat + (j & 1) * 256 + part * 64);
+        const float4* lse = reinterpret_cast<const float4*>(sm_stat + (j & 1) * 256 + part * kC);
         const float4* dd = lse + 32;
         if (!mbar_wait(&s_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(s_col, p);
-        uint32_t pk[32];
+        tmem_ld_cols<kC>(lane_base, p);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+        for (int i = 0; i < kC; i += 4) {
           const float4 m = lse[i >> 2];
           ffma2(p[i], p[i + 1], p[i], p[i + 1], sl2, sl2, -m.x, -m.y);
           ffma2(p[i + 2], p[i + 3], p[i + 2], p[i + 3], sl2, sl2, -m.z, -m.w);
@@ -702,50 +734,42 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           pk[i >> 1] = pack_bf16(p[i], p[i + 1]);
           pk[(i >> 1) + 1] = pack_bf16(p[i + 2], p[i + 3]);
         }
-        tmem_st32(s_col, reinterpret_cast<const float*>(pk));
-        tc_fence_before();
-        mbar_arrive(p_ready);
+        hand_over(lane_base, p_ready);
         if (!mbar_wait(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(dp_col, d);
+        tmem_ld_cols<kC>(lane_base + 128, d);
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+        for (int i = 0; i < kC; i += 4) {
           const float4 m = dd[i >> 2];
           pk[i >> 1] = pack_bf16(p[i] * (d[i] - m.x), p[i + 1] * (d[i + 1] - m.y));
           pk[(i >> 1) + 1] = pack_bf16(p[i + 2] * (d[i + 2] - m.z), p[i + 3] * (d[i + 3] - m.w));
         }
-        tmem_st32(dp_col, reinterpret_cast<const float*>(pk));
-        tc_fence_before();
-        mbar_arrive(ds_ready);
+        hand_over(lane_base + 128, ds_ready);
       }
     } else {
       const float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
       const float lse = stat[rloc], dd = stat[128 + rloc];
-      const uint32_t s_col = lane_base + part * 64, dp_col = lane_base + 256 + part * 64;
       for (int j = 0; j < n; ++j) {
         if (!mbar_wait(&s_full[j & 1], (j >> 1) & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(s_col + (j & 1) * 128, p);
+        tmem_ld_cols<kC>(lane_base + (j & 1) * 128, p);
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
+        for (int i = 0; i < kC; i += 2) {
           ffma2(p[i], p[i + 1], p[i], p[i + 1], sl2, sl2, -lse, -lse);
           p[i] = fast_exp2(p[i]);
           p[i + 1] = fast_exp2(p[i + 1]);
         }
-        const int lim = seq.valid(seq.used_slot(j)) - part * 64;
-        if (lim < 64) {
+        const int lim = seq.valid(seq.used_slot(j)) - part * kC;
+        if (lim < kC) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) p[i] = i < lim ? p[i] : 0.f;
+          for (int i = 0; i < kC; ++i) p[i] = i < lim ? p[i] : 0.f;
         }
         if (!mbar_wait(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld64(dp_col, d);
-        uint32_t pk[32];
+        tmem_ld_cols<kC>(lane_base + 256, d);
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) pk[i >> 1] = pack_bf16(p[i] * (d[i] - dd), p[i + 1] * (d[i + 1] - dd));
-        tmem_st32(dp_col, reinterpret_cast<const float*>(pk));
-        tc_fence_before();
-        mbar_arrive(ds_ready);
+        for (int i = 0; i < kC; i += 2) pk[i >> 1] = pack_bf16(p[i] * (d[i] - dd), p[i + 1] * (d[i + 1] - dd));
+        hand_over(lane_base + 256, ds_ready);
       }
     }
     if (ok && (n == 0 || mbar_wait(done, 0, 0x41c))) {
@@ -753,10 +777,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const bool own = rloc < seq.extent(slot);
       const int row = start + rloc;
       auto write = [&](const HeadsView& view, uint32_t col, float f) {
-        if (n > 0) tmem_ld64(lane_base + col + part * 64, d);
-        __nv_bfloat16* dst = head_row(view, b, head, row) + part * 64;
-        if (rloc < valid) store_bf16<64>(dst, d, f);
-        else if (own) store_zero<64>(dst);
+        if (n > 0) tmem_ld_cols<kC>(lane_base + col, d);
+        __nv_bfloat16* dst = head_row(view, b, head, row) + part * kC;
+        if (rloc < valid) store_bf16<kC>(dst, d, f);
+        else if (own) store_zero<kC>(dst);
       };
       if (is_kv) {
         write(a.dv, 256, 1.0f);
@@ -818,7 +842,7 @@ int launch_attention_backward(const AttnTrainArgs& a, cudaStream_t s) {
   note_launch();
   if (e == cudaSuccess) {
     const int blocks = a.slots * (a.kv_heads + a.heads) * a.batch;
-    e = launch_kernel(attn_train_bwd_kernel, dim3(blocks), dim3(kAtThreads), kBwdSmem, s, 1, mq, mk, mv, md, a);
+    e = launch_kernel(attn_train_bwd_kernel, dim3(blocks), dim3(kBwdThreads), kBwdSmem, s, 1, mq, mk, mv, md, a);
     note_launch();
   }
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;
