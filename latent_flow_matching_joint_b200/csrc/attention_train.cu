@@ -47,10 +47,16 @@ constexpr int kFwdSmem = kFwdBar + 256 + 1024;
 constexpr int kBwdWarps = KLEIN_BWD_WARPS;         // elementwise warps of the backward kernel
 constexpr int kBwdThreads = 64 + 32 * kBwdWarps;
 constexpr int kBwdCols = 128 / (kBwdWarps / 4);    // columns of a tile per warp
-constexpr int kBwdStat = 6 * kAtTile;    // 2 resident tiles, 2 stages of 2 streamed tiles, then 2 stages of statistics
+// Shared memory: 2 resident tiles, a ring of 3 of the first streamed tile (it
+// is needed from the scores to the end of its step, and the next step's scores
+// are made half a step ahead), a ring of 2 of the second, with the statistics.
+constexpr int kBwdRingS = 2 * kAtTile;
+constexpr int kBwdRingT = 5 * kAtTile;
+constexpr int kBwdStat = 7 * kAtTile;
 constexpr int kStatBytes = 2 * 128 * 4;
 constexpr int kBwdBar = kBwdStat + 2 * kStatBytes;
-constexpr int kBwdSmem = kBwdBar + 256 + 1024;
+constexpr int kBwdSmem = kBwdBar + 256;
+static_assert(kBwdSmem <= 227 * 1024, "shared memory of one CTA");
 
 // Descriptor of 16 rows of a tile as the contraction (the operand's own index,
 // d, is the contiguous one): next 64 d one box later, next 8 rows 1 KB later.
@@ -501,25 +507,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_train_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                           const AttnTrainArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sm_x = smem;                    // resident: K (Q in a dQ block)
   uint8_t* sm_y = smem + kAtTile;          // resident: V (dO)
-  uint8_t* sm_s = smem + 2 * kAtTile;      // [2 stages]: Q (K)
-  uint8_t* sm_t = smem + 4 * kAtTile;      // [2 stages]: dO (V)
-  float* sm_stat = reinterpret_cast<float*>(smem + kBwdStat);  // [2 stages][lse 128 | D 128], dK/dV blocks
+  uint8_t* sm_s = smem + kBwdRingS;        // [3]: Q (K)
+  uint8_t* sm_t = smem + kBwdRingT;        // [2]: dO (V)
+  float* sm_stat = reinterpret_cast<float*>(smem + kBwdStat);  // [2][lse 128 | D 128], dK/dV blocks
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBwdBar);
   uint64_t* x_full = bars + 0;
-  uint64_t* s_in = bars + 1;       // [2] first streamed tile (with the statistics)
-  uint64_t* t_in = bars + 3;       // [2] second streamed tile
-  uint64_t* st_empty = bars + 5;   // [2]
-  uint64_t* s_full = bars + 7;     // [2] scores ready (dK/dV blocks use the first)
-  uint64_t* dp_full = bars + 9;
-  uint64_t* p_ready = bars + 10;   // P in tensor memory (dK/dV blocks)
-  uint64_t* ds_ready = bars + 11;
-  uint64_t* done = bars + 12;
-  uint64_t* scrub = bars + 13;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  uint64_t* s_in = bars + 1;       // [3] first streamed tile
+  uint64_t* s_empty = bars + 4;    // [3]
+  uint64_t* t_in = bars + 7;       // [2] second streamed tile and the statistics
+  uint64_t* t_empty = bars + 9;    // [2] the tile
+  uint64_t* stat_empty = bars + 11;  // [2] the statistics, read until dS has been made
+  uint64_t* s_full = bars + 13;    // [2] scores ready (dK/dV blocks use the first)
+  uint64_t* dp_full = bars + 15;
+  uint64_t* p_ready = bars + 16;   // P in tensor memory (dK/dV blocks)
+  uint64_t* ds_ready = bars + 17;
+  uint64_t* done = bars + 18;
+  uint64_t* scrub = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -535,10 +542,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (warp == 0 && lane == 0) {
     mbar_init(x_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 3; ++s) {
       mbar_init(&s_in[s], 1);
+      mbar_init(&s_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&t_in[s], 1);
-      mbar_init(&st_empty[s], 1);
+      mbar_init(&t_empty[s], 1);
+      mbar_init(&stat_empty[s], kBwdWarps);
       mbar_init(&s_full[s], 1);
     }
     mbar_init(dp_full, 1);
@@ -579,69 +590,89 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const CUtensorMap* ms = is_kv ? &map_q : &map_k;
       const CUtensorMap* mt = is_kv ? &map_do : &map_v;
       int scrubs = 0;
+      int ss = 0;            // stage and phase of the first ring
+      uint32_t sp = 0;
       for (int j = 0; j < n; ++j) {
         const int st = j & 1;
-        const uint32_t phase = (j >> 1) & 1;
+        const uint32_t tp = (j >> 1) & 1;
         const int h = is_kv ? head * group + j / used : head / group;
         const int from = seq.used_slot(is_kv ? j % used : j);
         const int row = seq.start(from);
         const bool ragged = seq.ragged(from);
-        if (!mbar_wait(&st_empty[st], phase ^ 1, 0x411)) break;
+        const uint32_t second = kAtTile + (is_kv ? kStatBytes : 0);
+        uint64_t* sb = ragged ? scrub : &s_in[ss];
+        uint64_t* tb = ragged ? scrub : &t_in[st];
+        if (!mbar_wait(&s_empty[ss], sp ^ 1, 0x411)) break;
         if (lane == 0) {
-          const uint32_t first = kAtTile + (is_kv ? kStatBytes : 0);
-          uint64_t* sb = ragged ? scrub : &s_in[st];
-          uint64_t* tb = ragged ? scrub : &t_in[st];
-          if (ragged) {
-            mbar_arrive_expect_tx(scrub, first + kAtTile);
-          } else {
-            mbar_arrive_expect_tx(&s_in[st], first);
-            slog.armed(st, phase);
-            mbar_arrive_expect_tx(&t_in[st], kAtTile);
-            tlog.armed(st, phase);
-          }
-          if (is_kv)
-            bulk_load(sm_stat + st * 256, a.stats + ((static_cast<long long>(b) * a.heads + h) * a.slots + from) * 256,
-                      kStatBytes, sb);
-          tile_load(sm_s + st * kAtTile, ms, sb, row, h, b);
-          tile_load(sm_t + st * kAtTile, mt, tb, row, h, b);
-        }
-        if (ragged) {  // rows not in use are summed over by the products: zeros
-          __syncwarp();
-          if (!mbar_wait(scrub, scrubs & 1, 0x41b)) break;
-          ++scrubs;
-          scrub_rows(sm_s + st * kAtTile, seq.valid(from), lane);
-          scrub_rows(sm_t + st * kAtTile, seq.valid(from), lane);
-          if (lane == 0) {
-            mbar_arrive(&s_in[st]);
-            mbar_arrive(&t_in[st]);
-            slog.armed(st, phase);  // the logs hold each stage's latest phase
-            tlog.armed(st, phase);
-          }
+          mbar_arrive_expect_tx(sb, kAtTile + (ragged ? second : 0));
+          if (!ragged) slog.armed(ss, sp);
+          tile_load(sm_s + ss * kAtTile, ms, sb, row, h, b);
         }
         __syncwarp();
+        if (!mbar_wait(&t_empty[st], tp ^ 1, 0x41d)) break;
+        if (lane == 0) {
+          if (!ragged) {
+            mbar_arrive_expect_tx(tb, second);
+            tlog.armed(st, tp);
+          }
+          tile_load(sm_t + st * kAtTile, mt, tb, row, h, b);
+        }
+        __syncwarp();
+        if (is_kv) {
+          if (!mbar_wait(&stat_empty[st], tp ^ 1, 0x41e)) break;
+          if (lane == 0)
+            bulk_load(sm_stat + st * 256, a.stats + ((static_cast<long long>(b) * a.heads + h) * a.slots + from) * 256,
+                      kStatBytes, tb);
+          __syncwarp();
+        }
+        if (ragged) {  // rows not in use are summed over by the products: zeros
+          if (!mbar_wait(scrub, scrubs & 1, 0x41b)) break;
+          ++scrubs;
+          scrub_rows(sm_s + ss * kAtTile, seq.valid(from), lane);
+          scrub_rows(sm_t + st * kAtTile, seq.valid(from), lane);
+          if (lane == 0) {
+            mbar_arrive(&s_in[ss]);
+            mbar_arrive(&t_in[st]);
+            slog.armed(ss, sp);  // the logs hold each stage's latest phase
+            tlog.armed(st, tp);
+          }
+          __syncwarp();
+        }
+        if (++ss == 3) { ss = 0; sp ^= 1; }
       }
       // no TMA write may land in shared memory after the CTA exits
       if (lane == 0 && mbar_wait(x_full, 0, 0x419)) {
-        slog.drain(s_in, 2, 0x419);
+        slog.drain(s_in, 3, 0x419);
         tlog.drain(t_in, 2, 0x419);
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && n > 0) {
       bool ok = mbar_wait(x_full, 0, 0x412);
-      auto wait_in = [&](uint64_t* bar, int j) {
-        const bool r = mbar_wait(&bar[j & 1], (j >> 1) & 1, 0x413);
+      int si = 0, su = 0;  // first ring: stage of the next tile to wait for, of the step's tile
+      uint32_t sp = 0;
+      auto wait_s = [&]() -> const uint8_t* {  // the next first tile, or null
+        if (!mbar_wait(&s_in[si], sp, 0x413)) return nullptr;
+        tc_fence_after();
+        const uint8_t* tile = sm_s + si * kAtTile;
+        if (++si == 3) { si = 0; sp ^= 1; }
+        return tile;
+      };
+      auto wait_t = [&](int j) {
+        const bool r = mbar_wait(&t_in[j & 1], (j >> 1) & 1, 0x413);
         if (r) tc_fence_after();
         return r;
       };
+      const uint32_t t_s = tmem_base;
+      const uint8_t* tile = nullptr;
+      ok = ok && (tile = wait_s()) != nullptr;
+      if (ok) {
+        mma_along(t_s, sm_x, tile);
+        umma_commit(&s_full[0]);
+        ok = wait_t(0);
+      }
       if (is_kv) {
-        const uint32_t t_s = tmem_base, t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 384;
-        ok = ok && wait_in(s_in, 0);
-        if (ok) {
-          mma_along(t_s, sm_x, sm_s);
-          umma_commit(&s_full[0]);
-          ok = wait_in(t_in, 0);
-        }
+        const uint32_t t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 384;
         if (ok) {
           mma_along(t_dp, sm_y, sm_t);
           umma_commit(dp_full);
@@ -651,48 +682,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!mbar_wait(p_ready, j & 1, 0x414)) break;
           tc_fence_after();
           mma_across_bwd(t_dv, t_s, sm_t + st * kAtTile, j > 0);
+          umma_commit(&t_empty[st]);
           if (j + 1 < n) {
-            if (!wait_in(s_in, j + 1)) break;
-            mma_along(t_s, sm_x, sm_s + nx * kAtTile);
+            if (!(tile = wait_s())) break;
+            mma_along(t_s, sm_x, tile);
             umma_commit(&s_full[0]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x415)) break;
           tc_fence_after();
-          mma_across_bwd(t_dk, t_dp, sm_s + st * kAtTile, j > 0);
-          umma_commit(&st_empty[st]);
+          mma_across_bwd(t_dk, t_dp, sm_s + su * kAtTile, j > 0);
+          umma_commit(&s_empty[su]);
+          if (++su == 3) su = 0;
           if (j + 1 < n) {
-            if (!wait_in(t_in, j + 1)) break;
+            if (!wait_t(j + 1)) break;
             mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
             umma_commit(dp_full);
           }
         }
       } else {
-        const uint32_t t_s = tmem_base, t_dp = tmem_base + 256, t_dq = tmem_base + 384;
-        ok = ok && wait_in(s_in, 0);
-        if (ok) {
-          mma_along(t_s, sm_x, sm_s);
-          umma_commit(&s_full[0]);
-          ok = wait_in(t_in, 0);
-        }
+        const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
         if (ok) {
           mma_along(t_dp, sm_y, sm_t);
           umma_commit(dp_full);
+          umma_commit(&t_empty[0]);
         }
         for (int j = 0; ok && j < n; ++j) {
-          const int st = j & 1, nx = (j + 1) & 1;
+          const int nx = (j + 1) & 1;
           if (j + 1 < n) {  // the buffer of S_{j-1}, which dS_{j-1} was made from
-            if (!wait_in(s_in, j + 1)) break;
-            mma_along(t_s + nx * 128, sm_x, sm_s + nx * kAtTile);
+            if (!(tile = wait_s())) break;
+            mma_along(t_s + nx * 128, sm_x, tile);
             umma_commit(&s_full[nx]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x416)) break;
           tc_fence_after();
-          mma_across_bwd(t_dq, t_dp, sm_s + st * kAtTile, j > 0);
-          umma_commit(&st_empty[st]);
+          mma_across_bwd(t_dq, t_dp, sm_s + su * kAtTile, j > 0);
+          umma_commit(&s_empty[su]);
+          if (++su == 3) su = 0;
           if (j + 1 < n) {
-            if (!wait_in(t_in, j + 1)) break;
+            if (!wait_t(j + 1)) break;
             mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
             umma_commit(dp_full);
+            umma_commit(&t_empty[nx]);
           }
         }
       }
@@ -718,10 +748,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     };
     if (is_kv) {
       for (int j = 0; j < n; ++j) {
-        // the statistics came with the first streamed tile, which S^T has been made from
+        // the statistics come with the second streamed tile
         const float4* lse = reinterpret_cast<const float4*>(sm_stat + (j & 1) * 256 + part * kC);
         const float4* dd = lse + 32;
-        if (!mbar_wait(&s_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
+        if (!mbar_wait(&t_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base, p);
 #pragma unroll
@@ -745,6 +775,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           pk[(i >> 1) + 1] = pack_bf16(p[i + 2] * (d[i + 2] - m.z), p[i + 3] * (d[i + 3] - m.w));
         }
         hand_over(lane_base + 128, ds_ready);
+        if (lane == 0) mbar_arrive(&stat_empty[j & 1]);
       }
     } else {
       const float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
