@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      if (lane == 0) mbar_arrive_cluster_tmem(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     };
     auto fetch_res = [&](int row0, int col) {  // lane 0: a round's residual, into boxes that nothing uses
       lin_bulk_wait_read();
