@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kAtTile = 128 * 128 * 2;   // 128 rows x 128 d, bf16: two boxes of 64 d, 16 KB each
 constexpr int kAtBox = kAtTile / 2;
-constexpr int kAtHalfBox = kAtBox / 2;   // 64 rows of it
 constexpr int kAtThreads = 320;
 constexpr uint32_t kAtTmem = 512;
 constexpr float kAtRescale = 8.0f;       // log2 units: the running maximum moves only when a row's maximum grows by > 2^8
@@ -88,25 +87,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// (d within a half, row, half of d, head, item)
-__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int c1, int c2, int c3,
-                                            int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int c1, int c2,
-                                                 int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-      : "memory");
-}
-
 __device__ __forceinline__ void tile_load(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int head, int b) {
   tma_load_4d(dst, map, bar, 0, row, head, b);
   tma_load_4d(dst + kAtBox, map, bar, 64, row, head, b);
@@ -118,22 +98,6 @@ __device__ __forceinline__ void scrub_rows(uint8_t* tile, int valid, int lane) {
   for (int i = lane; i < 2 * chunks; i += 32) {
     const int box = i >= chunks;
     *reinterpret_cast<uint4*>(tile + box * kAtBox + valid * 128 + (i - box * chunks) * 16) = make_uint4(0, 0, 0, 0);
-  }
-  fence_async_smem();
-  __syncwarp();
-}
-
-// A streamed tile of a pair lies in each CTA as two parts of 16 KB, one load
-// each (TMA spends about 150 clocks on a load besides 64 bytes a clock: 8 KB
-// loads were the pair's bottleneck): rows 64 rank.. of all d, [2 halves of
-// d][64 rows][64 d], and all rows of d 64 rank.., [128 rows][64 d].
-
-// Zeroes what is past row `valid` of the tile in those parts; the whole warp takes part.
-__device__ __forceinline__ void scrub_parts(uint8_t* tile, int valid, int rank, int lane) {
-  for (int i = lane; i < kAtTile / 16; i += 32) {
-    const int r = (i >> 3) & 63, part = i >> 9;
-    const int row = part < 2 ? 64 * rank + r : 64 * (part - 2) + r;
-    if (row >= valid) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
   __syncwarp();
@@ -195,32 +159,15 @@ __device__ __forceinline__ void mma_across_half(uint32_t d_tmem, uint32_t a_tmem
     umma_bf16_tmem_a(d_tmem, a_tmem + kk * 8, across_desc(b0 + kk * 2048), kIdescAcross, accumulate || kk != 0);
 }
 
-// ---- products of a CTA pair: each CTA has its own 128 rows of A and of the
-// result, and half of B: 64 of its 128 rows for the scores, 64 of its 128
-// columns (d) for the products across the contraction.
-
-constexpr uint32_t kIdescPairAlong = idesc_bf16_f32(256, 128);
-constexpr uint32_t kIdescPairAcross = kIdescPairAlong | (1u << 16);
-
-// Scores: A a resident tile [128 rows][128 d], B the first half of a streamed tile: [64 rows][128 d].
-__device__ __forceinline__ void mma_along_pair(uint32_t d_tmem, const uint8_t* a, const uint8_t* b) {
-  const uint32_t a0 = smem_u32(a), b0 = smem_u32(b);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_bf16_pair(d_tmem, sw128_desc(a0 + (kk >> 2) * kAtBox + (kk & 3) * 32),
-                   sw128_desc(b0 + (kk >> 2) * kAtHalfBox + (kk & 3) * 32), kIdescPairAlong, kk != 0);
-}
-
-// A packed bf16 in tensor memory as the backward kernel's warps leave it (each
-// kBwdCols columns' values at the start of those columns), B the second half
-// of a streamed tile: [128 rows][64 d].
-__device__ __forceinline__ void mma_across_pair(uint32_t d_tmem, uint32_t a_tmem, const uint8_t* b, bool accumulate) {
-  const uint32_t b0 = smem_u32(b) + kAtTile / 2;
+// The whole contraction, A as the backward kernel's warps leave it: each
+// kBwdCols columns' packed values at the start of those columns.
+__device__ __forceinline__ void mma_across_bwd(uint32_t d_tmem, uint32_t a_tmem, const uint8_t* b, bool accumulate) {
+  const uint32_t b0 = smem_u32(b);
   constexpr int kSteps = kBwdCols / 16;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    umma_bf16_pair_tmem_a(d_tmem, a_tmem + (kk / kSteps) * kBwdCols + (kk % kSteps) * 8, across_desc(b0 + kk * 2048),
-                          kIdescPairAcross, accumulate || kk != 0);
+    umma_bf16_tmem_a(d_tmem, a_tmem + (kk / kSteps) * kBwdCols + (kk % kSteps) * 8, across_desc(b0 + kk * 2048),
+                     kIdescAcross, accumulate || kk != 0);
 }
 
 template <int N>
@@ -537,108 +484,91 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
   }
 }
 
-// Backward. The first CTA pairs make dK and dV, two key slots of one key head
+// Backward. The first blocks make dK and dV, one key slot of one key head
 // each, going through the query slots of every query head that shares it; the
-// rest make dQ, two query slots of one head each, going through the key slots.
+// rest make dQ, one query slot of one head each, going through the key slots.
 // Recomputing the scores in both costs 7 products instead of 5, but no sum
-// is shared between pairs: no atomics, no fp32 copy of dQ in memory, and the
+// is shared between blocks: no atomics, no fp32 copy of dQ in memory, and the
 // same bits every run. Both kinds are one grid, so that the second fills the
 // SMs that the first leaves at its end.
 //
-// A pair, because shared memory bounds one CTA: a 128 x 128 x 128 product
-// with both operands there reads 64 KB in its 512 clocks, all that shared
-// memory delivers, next to 64 KB of loads per step. A pair's product reads half
-// of B in each CTA.
+// Roles (320 threads): warp 0 TMA, warp 1 MMA issue, warps 2..9 elementwise,
+// two per TMEM lane quarter, each with half of the tile's columns. P and dS are
+// packed to bf16 over the scores they came from (each warp over its own
+// columns) and fed to the next product from tensor memory.
 //
-// Roles (576 threads): warp 0 TMA, warp 1 MMA issue (of the even CTA), warps
-// 2..17 elementwise, four per TMEM lane quarter, each with 32 of the tile's
-// columns. P and dS are packed to bf16 over the scores they came from (each
-// warp over its own columns) and fed to the next product from tensor memory.
-//
-// dK/dV pair: lanes are keys, columns queries. S^T = K Q^T and dP^T = V dO^T;
+// dK/dV block: lanes are keys, columns queries. S^T = K Q^T and dP^T = V dO^T;
 // dV += P^T dO, dK += dS^T Q. Tensor memory: S^T | dP^T | dV | dK, 128 columns
 // each. While the warps make P_j the tensor core runs dK_{j-1} and dP_j;
 // while they make dS_j it runs dV_j and S_{j+1}.
-// dQ pair: lanes are queries, columns keys. S = Q K^T (two buffers), dP = dO V^T,
+// dQ block: lanes are queries, columns keys. S = Q K^T (two buffers), dP = dO V^T,
 // dQ += dS K.
-struct BwdMaps {  // of q, k, v, dout: boxes of 64 rows x both halves of d, and of 128 rows x one half
-  CUtensorMap half_q, half_k, half_v, half_do, col_q, col_k, col_v, col_do;
-};
-
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_train_bwd_kernel(const __grid_constant__ BwdMaps maps, const AttnTrainArgs a) {
+    attn_train_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                          const AttnTrainArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sm_x = smem;                    // resident: K (Q in a dQ pair), this CTA's slot
+  uint8_t* sm_x = smem;                    // resident: K (Q in a dQ block)
   uint8_t* sm_y = smem + kAtTile;          // resident: V (dO)
-  uint8_t* sm_s = smem + kBwdRingS;        // [3]: Q (K), this CTA's parts
+  uint8_t* sm_s = smem + kBwdRingS;        // [3]: Q (K)
   uint8_t* sm_t = smem + kBwdRingT;        // [2]: dO (V)
-  float* sm_stat = reinterpret_cast<float*>(smem + kBwdStat);  // [2][lse 128 | D 128], dK/dV pairs
+  float* sm_stat = reinterpret_cast<float*>(smem + kBwdStat);  // [2][lse 128 | D 128], dK/dV blocks
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBwdBar);
-  // the even CTA's, for both: one arrival of each producer, and both CTAs' bytes
   uint64_t* x_full = bars + 0;
   uint64_t* s_in = bars + 1;       // [3] first streamed tile
-  uint64_t* t_in = bars + 4;       // [2] second streamed tile
-  // the even CTA's, one arrival of each elementwise warp of both
-  uint64_t* p_ready = bars + 6;    // P in tensor memory (dK/dV pairs)
-  uint64_t* ds_ready = bars + 7;
-  // each CTA's own, arrived on by the products of the pair
-  uint64_t* s_empty = bars + 8;    // [3]
-  uint64_t* t_empty = bars + 11;   // [2]
-  uint64_t* s_full = bars + 13;    // [2] scores ready (dK/dV pairs use the first)
+  uint64_t* s_empty = bars + 4;    // [3]
+  uint64_t* t_in = bars + 7;       // [2] second streamed tile and the statistics
+  uint64_t* t_empty = bars + 9;    // [2] the tile
+  uint64_t* stat_empty = bars + 11;  // [2] the statistics, read until dS has been made
+  uint64_t* s_full = bars + 13;    // [2] scores ready (dK/dV blocks use the first)
   uint64_t* dp_full = bars + 15;
-  uint64_t* done = bars + 16;
-  // each CTA's own
-  uint64_t* stat_in = bars + 17;     // [2]
-  uint64_t* stat_empty = bars + 19;  // [2]
-  uint64_t* scrub = bars + 21;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
+  uint64_t* p_ready = bars + 16;   // P in tensor memory (dK/dV blocks)
+  uint64_t* ds_ready = bars + 17;
+  uint64_t* done = bars + 18;
+  uint64_t* scrub = bars + 19;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const bool leader = rank == 0;
-  const int slot_pairs = (a.slots + 1) >> 1;
-  const int kv_pairs = slot_pairs * a.kv_heads * a.batch;
-  const int pair = blockIdx.x >> 1;
-  const bool is_kv = pair < kv_pairs;
+  const int kv_blocks = a.slots * a.kv_heads * a.batch;
+  const bool is_kv = static_cast<int>(blockIdx.x) < kv_blocks;
   const int group = a.heads / a.kv_heads;
-  const int pid = is_kv ? pair : pair - kv_pairs;
-  const int slot0 = 2 * (pid % slot_pairs), slot = slot0 + rank;
-  const int bh = pid / slot_pairs;
+  const int bid = is_kv ? blockIdx.x : blockIdx.x - kv_blocks;
+  const int slot = bid % a.slots;
+  const int bh = bid / a.slots;
   const int n_heads = is_kv ? a.kv_heads : a.heads;
-  const int head = bh % n_heads;  // key head (query head in a dQ pair)
+  const int head = bh % n_heads;  // key head (query head in a dQ block)
   const int b = bh / n_heads;
 
   if (warp == 0 && lane == 0) {
-    mbar_init(x_full, 2);
+    mbar_init(x_full, 1);
     for (int s = 0; s < 3; ++s) {
-      mbar_init(&s_in[s], 2);
+      mbar_init(&s_in[s], 1);
       mbar_init(&s_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&t_in[s], 2);
+      mbar_init(&t_in[s], 1);
       mbar_init(&t_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&stat_in[s], 1);
       mbar_init(&stat_empty[s], kBwdWarps);
+      mbar_init(&s_full[s], 1);
     }
-    mbar_init(p_ready, 2 * kBwdWarps);
-    mbar_init(ds_ready, 2 * kBwdWarps);
     mbar_init(dp_full, 1);
+    mbar_init(p_ready, kBwdWarps);
+    mbar_init(ds_ready, kBwdWarps);
     mbar_init(done, 1);
     mbar_init(scrub, 1);
     fence_barrier_init();
-    tma_prefetch_desc(is_kv ? &maps.col_k : &maps.col_q);
-    tma_prefetch_desc(is_kv ? &maps.col_v : &maps.col_do);
-    tma_prefetch_desc(is_kv ? &maps.half_q : &maps.half_k);
-    tma_prefetch_desc(is_kv ? &maps.half_do : &maps.half_v);
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_do);
   }
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, kAtTmem);
-    tmem_relinquish_pair();
+    tmem_alloc(tmem_slot, kAtTmem);
+    tmem_relinquish();
   }
   tc_fence_before();
-  cluster_sync();  // barrier initialisation and the TMEM allocation are visible pair-wide
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_trigger();
@@ -647,29 +577,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Slots seq(a, b);
   const int valid = seq.valid(slot), start = seq.start(slot);
   const int used = seq.used();
-  // steps; none when neither CTA has a row in use
-  const int n = seq.valid(slot0) + seq.valid(slot0 + 1) > 0 ? (is_kv ? used * group : used) : 0;
+  const int n = valid > 0 ? (is_kv ? used * group : used) : 0;
 
   if (warp == 0) {
     if (n > 0) {
-      // One arrival on a barrier of the even CTA, and there the bytes to expect from both CTAs.
-      auto expect = [&](uint64_t* bar, uint32_t bytes) {
-        if (leader) mbar_arrive_expect_tx(bar, 2 * bytes);
-        else mbar_arrive_cluster_tmem(mapa_shared(smem_u32(bar), 0));  // (publishes nothing: the bytes count)
-      };
       StageLog slog, tlog;
       if (lane == 0) {
-        expect(x_full, 2 * kAtTile);
-        const uint32_t bar = mapa_shared(smem_u32(x_full), 0);
-        for (int i = 0; i < 2; ++i) {
-          tma_load_5d_pair(sm_x + i * kAtBox, is_kv ? &maps.col_k : &maps.col_q, bar, start, i, head, b);
-          tma_load_5d_pair(sm_y + i * kAtBox, is_kv ? &maps.col_v : &maps.col_do, bar, start, i, head, b);
-        }
+        mbar_arrive_expect_tx(x_full, 2 * kAtTile);
+        tile_load(sm_x, is_kv ? &map_k : &map_q, x_full, start, head, b);
+        tile_load(sm_y, is_kv ? &map_v : &map_do, x_full, start, head, b);
       }
-      const CUtensorMap* half_s = is_kv ? &maps.half_q : &maps.half_k;
-      const CUtensorMap* half_t = is_kv ? &maps.half_do : &maps.half_v;
-      const CUtensorMap* col_s = is_kv ? &maps.col_q : &maps.col_k;
-      const uint32_t t_bytes = is_kv ? kAtTile : kAtTile / 2;  // V is only read along d
+      const CUtensorMap* ms = is_kv ? &map_q : &map_k;
+      const CUtensorMap* mt = is_kv ? &map_do : &map_v;
       int scrubs = 0;
       int ss = 0;            // stage and phase of the first ring
       uint32_t sp = 0;
@@ -680,51 +599,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int from = seq.used_slot(is_kv ? j % used : j);
         const int row = seq.start(from);
         const bool ragged = seq.ragged(from);
-        uint8_t* s_tile = sm_s + ss * kAtTile;
-        uint8_t* t_tile = sm_t + st * kAtTile;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int r, int d_half) {
-          if (ragged) tma_load_5d(dst, map, scrub, r, d_half, h, b);
-          else tma_load_5d_pair(dst, map, mapa_shared(smem_u32(bar), 0), r, d_half, h, b);
-        };
+        const uint32_t second = kAtTile + (is_kv ? kStatBytes : 0);
+        uint64_t* sb = ragged ? scrub : &s_in[ss];
+        uint64_t* tb = ragged ? scrub : &t_in[st];
         if (!mbar_wait(&s_empty[ss], sp ^ 1, 0x411)) break;
         if (lane == 0) {
-          if (ragged) {
-            mbar_arrive_expect_tx(scrub, kAtTile + t_bytes);
-          } else {
-            expect(&s_in[ss], kAtTile);
-            slog.armed(ss, sp);
-          }
-          load(s_tile, half_s, &s_in[ss], row + 64 * rank, 0);
-          load(s_tile + kAtBox, col_s, &s_in[ss], row, rank);
+          mbar_arrive_expect_tx(sb, kAtTile + (ragged ? second : 0));
+          if (!ragged) slog.armed(ss, sp);
+          tile_load(sm_s + ss * kAtTile, ms, sb, row, h, b);
         }
         __syncwarp();
         if (!mbar_wait(&t_empty[st], tp ^ 1, 0x41d)) break;
         if (lane == 0) {
           if (!ragged) {
-            expect(&t_in[st], t_bytes);
+            mbar_arrive_expect_tx(tb, second);
             tlog.armed(st, tp);
           }
-          load(t_tile, half_t, &t_in[st], row + 64 * rank, 0);
-          if (is_kv) load(t_tile + kAtBox, &maps.col_do, &t_in[st], row, rank);
+          tile_load(sm_t + st * kAtTile, mt, tb, row, h, b);
         }
         __syncwarp();
         if (is_kv) {
           if (!mbar_wait(&stat_empty[st], tp ^ 1, 0x41e)) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&stat_in[st], kStatBytes);
+          if (lane == 0)
             bulk_load(sm_stat + st * 256, a.stats + ((static_cast<long long>(b) * a.heads + h) * a.slots + from) * 256,
-                      kStatBytes, &stat_in[st]);
-          }
+                      kStatBytes, tb);
           __syncwarp();
         }
         if (ragged) {  // rows not in use are summed over by the products: zeros
           if (!mbar_wait(scrub, scrubs & 1, 0x41b)) break;
           ++scrubs;
-          scrub_parts(s_tile, seq.valid(from), rank, lane);
-          scrub_parts(t_tile, seq.valid(from), rank, lane);
+          scrub_rows(sm_s + ss * kAtTile, seq.valid(from), lane);
+          scrub_rows(sm_t + st * kAtTile, seq.valid(from), lane);
           if (lane == 0) {
-            mbar_arrive_cluster(mapa_shared(smem_u32(&s_in[ss]), 0));
-            mbar_arrive_cluster(mapa_shared(smem_u32(&t_in[st]), 0));
+            mbar_arrive(&s_in[ss]);
+            mbar_arrive(&t_in[st]);
             slog.armed(ss, sp);  // the logs hold each stage's latest phase
             tlog.armed(st, tp);
           }
@@ -732,19 +640,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (++ss == 3) { ss = 0; sp ^= 1; }
       }
-      // No TMA write may land in shared memory after the pair exits: the even
-      // CTA's barriers count both CTAs' bytes, and the cluster barrier below
-      // keeps the other CTA alive.
-      if (lane == 0 && leader && mbar_wait(x_full, 0, 0x419)) {
+      // no TMA write may land in shared memory after the CTA exits
+      if (lane == 0 && mbar_wait(x_full, 0, 0x419)) {
         slog.drain(s_in, 3, 0x419);
         tlog.drain(t_in, 2, 0x419);
       }
-      if (lane == 0 && is_kv) {  // (their last phases)
-        for (int i = n > 1 ? n - 2 : 0; i < n; ++i) mbar_wait(&stat_in[i & 1], (i >> 1) & 1, 0x419);
-      }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader && n > 0) {
+    if (lane == 0 && n > 0) {
       bool ok = mbar_wait(x_full, 0, 0x412);
       int si = 0, su = 0;  // first ring: stage of the next tile to wait for, of the step's tile
       uint32_t sp = 0;
@@ -760,72 +663,71 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (r) tc_fence_after();
         return r;
       };
-      auto commit = [](uint64_t* bar) { umma_commit_pair(bar, 0x3); };
       const uint32_t t_s = tmem_base;
       const uint8_t* tile = nullptr;
       ok = ok && (tile = wait_s()) != nullptr;
       if (ok) {
-        mma_along_pair(t_s, sm_x, tile);
-        commit(&s_full[0]);
+        mma_along(t_s, sm_x, tile);
+        umma_commit(&s_full[0]);
         ok = wait_t(0);
       }
       if (is_kv) {
         const uint32_t t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 384;
         if (ok) {
-          mma_along_pair(t_dp, sm_y, sm_t);
-          commit(dp_full);
+          mma_along(t_dp, sm_y, sm_t);
+          umma_commit(dp_full);
         }
         for (int j = 0; ok && j < n; ++j) {
           const int st = j & 1, nx = (j + 1) & 1;
           if (!mbar_wait(p_ready, j & 1, 0x414)) break;
           tc_fence_after();
-          mma_across_pair(t_dv, t_s, sm_t + st * kAtTile, j > 0);
-          commit(&t_empty[st]);
+          mma_across_bwd(t_dv, t_s, sm_t + st * kAtTile, j > 0);
+          umma_commit(&t_empty[st]);
           if (j + 1 < n) {
             if (!(tile = wait_s())) break;
-            mma_along_pair(t_s, sm_x, tile);
-            commit(&s_full[0]);
+            mma_along(t_s, sm_x, tile);
+            umma_commit(&s_full[0]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x415)) break;
           tc_fence_after();
-          mma_across_pair(t_dk, t_dp, sm_s + su * kAtTile, j > 0);
-          commit(&s_empty[su]);
+          mma_across_bwd(t_dk, t_dp, sm_s + su * kAtTile, j > 0);
+          umma_commit(&s_empty[su]);
           if (++su == 3) su = 0;
           if (j + 1 < n) {
             if (!wait_t(j + 1)) break;
-            mma_along_pair(t_dp, sm_y, sm_t + nx * kAtTile);
-            commit(dp_full);
+            mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
+            umma_commit(dp_full);
           }
         }
       } else {
         const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
         if (ok) {
-          mma_along_pair(t_dp, sm_y, sm_t);
-          commit(dp_full);
-          commit(&t_empty[0]);
+          mma_along(t_dp, sm_y, sm_t);
+          umma_commit(dp_full);
+          umma_commit(&t_empty[0]);
         }
         for (int j = 0; ok && j < n; ++j) {
           const int nx = (j + 1) & 1;
           if (j + 1 < n) {  // the buffer of S_{j-1}, which dS_{j-1} was made from
             if (!(tile = wait_s())) break;
-            mma_along_pair(t_s + nx * 128, sm_x, tile);
-            commit(&s_full[nx]);
+            mma_along(t_s + nx * 128, sm_x, tile);
+            umma_commit(&s_full[nx]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x416)) break;
           tc_fence_after();
-          mma_across_pair(t_dq, t_dp, sm_s + su * kAtTile, j > 0);
-          commit(&s_empty[su]);
+          mma_across_bwd(t_dq, t_dp, sm_s + su * kAtTile, j > 0);
+          umma_commit(&s_empty[su]);
           if (++su == 3) su = 0;
           if (j + 1 < n) {
             if (!wait_t(j + 1)) break;
-            mma_along_pair(t_dp, sm_y, sm_t + nx * kAtTile);
-            commit(dp_full);
-            commit(&t_empty[nx]);
+            mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
+            umma_commit(dp_full);
+            umma_commit(&t_empty[nx]);
           }
         }
       }
       // every MMA issued here has completed before the results are read and TMEM is freed
-      commit(done);
+      umma_commit(done);
       mbar_wait(done, 0, 0x41a);
     }
   } else {
@@ -838,20 +740,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     float p[kC], d[kC];
     uint32_t pk[kC / 2];
-    auto hand_over = [&](uint32_t col, uint64_t* bar) {  // the packed values, to the even CTA's MMA warp
+    auto hand_over = [&](uint32_t col, uint64_t* bar) {  // the packed values, to the MMA warp
       tmem_st_cols<kC / 2>(col, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(bar);
-        else mbar_arrive_cluster_tmem(mapa_shared(smem_u32(bar), 0));
-      }
+      if (lane == 0) mbar_arrive(bar);
     };
     if (is_kv) {
       for (int j = 0; j < n; ++j) {
+        // the statistics come with the second streamed tile
         const float4* lse = reinterpret_cast<const float4*>(sm_stat + (j & 1) * 256 + part * kC);
         const float4* dd = lse + 32;
-        if (!mbar_wait(&stat_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
+        if (!mbar_wait(&t_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base, p);
 #pragma unroll
@@ -878,12 +778,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) mbar_arrive(&stat_empty[j & 1]);
       }
     } else {
-      float lse = INFINITY, dd = 0.f;
-      if (slot < a.slots) {
-        const float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
-        lse = stat[rloc];
-        dd = stat[128 + rloc];
-      }
+      const float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
+      const float lse = stat[rloc], dd = stat[128 + rloc];
       for (int j = 0; j < n; ++j) {
         if (!mbar_wait(&s_full[j & 1], (j >> 1) & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
@@ -926,13 +822,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
 
-  __syncwarp();
   tc_fence_before();
-  cluster_sync();  // every MMA of the pair, and everything that arrives on the other CTA's barriers, is done
+  __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, kAtTmem);
+    tmem_dealloc(tmem_base, kAtTmem);
   }
 }
 
@@ -941,13 +836,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 static int make_heads_map(CUtensorMap* map, const HeadsView& v, int rows, int heads, int batch) {
   return make_map_4d(map, v.data, kHeadDim, rows, heads, batch, static_cast<uint64_t>(v.row_stride) * 2,
                      static_cast<uint64_t>(v.head_stride) * 2, static_cast<uint64_t>(v.batch_stride) * 2, 64, 128);
-}
-
-static int make_halves_map(CUtensorMap* map, const HeadsView& v, int rows, int heads, int batch, int box_rows,
-                           int box_halves) {
-  return make_map_5d(map, v.data, 64, rows, 2, heads, batch, static_cast<uint64_t>(v.row_stride) * 2, 128,
-                     static_cast<uint64_t>(v.head_stride) * 2, static_cast<uint64_t>(v.batch_stride) * 2, 64, box_rows,
-                     box_halves);
 }
 
 template <typename K>
@@ -977,24 +865,15 @@ int launch_attention_train(const AttnTrainArgs& a, cudaStream_t s) {
 int launch_attention_backward(const AttnTrainArgs& a, cudaStream_t s) {
   static bool configured[kMaxDevices] = {};
   if (opt_in_smem(attn_train_bwd_kernel, kBwdSmem, configured)) return -1;
-  BwdMaps m;
-  const struct {
-    CUtensorMap *half, *col;
-    const HeadsView* view;
-    int heads;
-  } each[4] = {{&m.half_q, &m.col_q, &a.q, a.heads},
-               {&m.half_k, &m.col_k, &a.k, a.kv_heads},
-               {&m.half_v, &m.col_v, &a.v, a.kv_heads},
-               {&m.half_do, &m.col_do, &a.dout, a.heads}};
-  for (const auto& t : each)
-    if (make_halves_map(t.half, *t.view, a.rows, t.heads, a.batch, 64, 2) ||
-        make_halves_map(t.col, *t.view, a.rows, t.heads, a.batch, 128, 1))
-      return -2;
+  CUtensorMap mq, mk, mv, md;
+  if (make_heads_map(&mq, a.q, a.rows, a.heads, a.batch) || make_heads_map(&mk, a.k, a.rows, a.kv_heads, a.batch) ||
+      make_heads_map(&mv, a.v, a.rows, a.kv_heads, a.batch) || make_heads_map(&md, a.dout, a.rows, a.heads, a.batch))
+    return -2;
   cudaError_t e = launch_kernel(attn_stat_kernel, dim3(a.slots, a.heads, a.batch), dim3(256), 0, s, 1, a);
   note_launch();
   if (e == cudaSuccess) {
-    const int pairs = (a.slots + 1) / 2 * (a.kv_heads + a.heads) * a.batch;
-    e = launch_kernel(attn_train_bwd_kernel, dim3(2 * pairs), dim3(kBwdThreads), kBwdSmem, s, 2, m, a);
+    const int blocks = a.slots * (a.kv_heads + a.heads) * a.batch;
+    e = launch_kernel(attn_train_bwd_kernel, dim3(blocks), dim3(kBwdThreads), kBwdSmem, s, 1, mq, mk, mv, md, a);
     note_launch();
   }
   return (e == cudaSuccess && cudaPeekAtLastError() == cudaSuccess) ? 0 : -1;

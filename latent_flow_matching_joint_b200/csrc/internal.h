@@ -19,9 +19,6 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t out
 // 3-D bf16 tensor map over [d2][d1][d0] with byte strides s1 (d1) and s2 (d2).
 int make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                 uint64_t s2, uint32_t box0, uint32_t box1, int bytes1 = 0);
-// 5-D, box = box0 x box1 x box2 x 1 x 1.
-int make_map_5d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t d4,
-                uint64_t s1, uint64_t s2, uint64_t s3, uint64_t s4, uint32_t box0, uint32_t box1, uint32_t box2);
 // 2-D map of rows of bf16 (or fp32) with pitch ld in elements; box 32 rows of 128 bytes, swizzled.
 int make_map_rows32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, int f32);
 // 4-D bf16 tensor map over [d3][d2][d1][d0] with byte strides s1..s3; box = box0 x box1 x 1 x 1.

@@ -170,19 +170,6 @@ int make_map_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, ui
   return r == CUDA_SUCCESS ? 0 : -1;
 }
 
-int make_map_5d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t d4,
-                uint64_t s1, uint64_t s2, uint64_t s3, uint64_t s4, uint32_t box0, uint32_t box1, uint32_t box2) {
-  if (get_encode()) return -1;
-  cuuint64_t dims[5] = {d0, d1, d2, d3, d4};
-  cuuint64_t strides[4] = {s1, s2, s3, s4};
-  cuuint32_t box[5] = {box0, box1, box2, 1, 1};
-  cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? 0 : -1;
-}
-
 // ------------------------------------------------------------------ workspace
 
 static inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1232,9 +1219,9 @@ static int check_attention_shape(const klein_attention_shape* s, AttnTrainArgs* 
   a->scale = s->scale;
   a->scale_log2 = static_cast<float>(1.4426950408889634 * s->scale);
   const long long slots = attn_slots(a->rows, a->n_txt);
-  // launch grids: (slots, heads, batch), and a block per slot (an even number of them) and head of either kind
+  // launch grids: (slots, heads, batch), and one block per slot and head of either kind
   if (a->rows > (1 << 30) || a->heads > 65535 || a->batch > 65535 ||
-      static_cast<double>(slots + 1) * (a->heads + a->kv_heads) * a->batch > 2147483647.0)
+      static_cast<double>(slots) * (a->heads + a->kv_heads) * a->batch > 2147483647.0)
     return fail(KLEIN_ERR_SHAPE, "too many rows, heads or batch items");
   a->slots = static_cast<int>(slots);
   return KLEIN_OK;
