@@ -141,11 +141,11 @@ struct Slots {
 // D[128 x 128] (+)= A[128 x 128] B[128 x 128]^T: both tiles contiguous along
 // the contraction (d).
 __device__ __forceinline__ void mma_along(uint32_t d_tmem, const uint8_t* a, const uint8_t* b) {
-  const uint32_t a0 = smem_u32(a), b0 = smem_u32(b);
+  const uint64_t da = sw128_desc(smem_u32(a)), db = sw128_desc(smem_u32(b));
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = (kk >> 2) * kAtBox + (kk & 3) * 32;
-    umma_bf16(d_tmem, sw128_desc(a0 + off), sw128_desc(b0 + off), kIdescAlong, kk != 0);
+    const uint32_t off = ((kk >> 2) * kAtBox + (kk & 3) * 32) >> 4;  // in the descriptors' 16-byte units
+    umma_bf16_warp(d_tmem, da + off, db + off, kIdescAlong, kk != 0);
   }
 }
 
@@ -153,21 +153,21 @@ __device__ __forceinline__ void mma_along(uint32_t d_tmem, const uint8_t* a, con
 // A in TMEM as packed bf16 from column a_tmem on.
 __device__ __forceinline__ void mma_across_half(uint32_t d_tmem, uint32_t a_tmem, const uint8_t* b, int half,
                                                 bool accumulate) {
-  const uint32_t b0 = smem_u32(b) + half * 4 * 2048;
+  const uint64_t db = across_desc(smem_u32(b) + half * 4 * 2048);
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
-    umma_bf16_tmem_a(d_tmem, a_tmem + kk * 8, across_desc(b0 + kk * 2048), kIdescAcross, accumulate || kk != 0);
+    umma_bf16_tmem_a_warp(d_tmem, a_tmem + kk * 8, db + kk * (2048 >> 4), kIdescAcross, accumulate || kk != 0);
 }
 
 // The whole contraction, A as the backward kernel's warps leave it: each
 // kBwdCols columns' packed values at the start of those columns.
 __device__ __forceinline__ void mma_across_bwd(uint32_t d_tmem, uint32_t a_tmem, const uint8_t* b, bool accumulate) {
-  const uint32_t b0 = smem_u32(b);
+  const uint64_t db = across_desc(smem_u32(b));
   constexpr int kSteps = kBwdCols / 16;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    umma_bf16_tmem_a(d_tmem, a_tmem + (kk / kSteps) * kBwdCols + (kk % kSteps) * 8, across_desc(b0 + kk * 2048),
-                     kIdescAcross, accumulate || kk != 0);
+    umma_bf16_tmem_a_warp(d_tmem, a_tmem + (kk / kSteps) * kBwdCols + (kk % kSteps) * 8, db + kk * (2048 >> 4),
+                          kIdescAcross, accumulate || kk != 0);
 }
 
 template <int N>
@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {  // the whole warp, see umma_bf16_warp
       auto issue_s = [&](int t, int j) {
         mma_along(tmem_base + t * 256, sm_q + t * kAtTile, sm_k + (j & 1) * kAtTile);
-        umma_commit(&s_full[t]);
+        umma_commit_warp(&s_full[t]);
       };
       bool ok = mbar_wait(q_full, 0, 0x402) && mbar_wait(&k_full[0], 0, 0x403);
       if (ok) {
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             (j | half) != 0);
           }
           if (!ok) break;
-          if (t == 1) umma_commit(&kv_empty[st]);
+          if (t == 1) umma_commit_warp(&kv_empty[st]);
           if (j + 1 < n) {
             if (t == 0) {
               if (!mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 0x406)) { ok = false; break; }
@@ -336,12 +336,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             issue_s(t, j + 1);
           } else {
-            umma_commit(&s_full[t]);  // output of slot t final
+            umma_commit_warp(&s_full[t]);  // output of slot t final
           }
         }
       }
       // every MMA issued here has completed before TMEM is freed
-      umma_commit(drain);
+      umma_commit_warp(drain);
       mbar_wait(drain, 0, 0x40a);
     }
   } else {
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {  // the whole warp, see umma_bf16_warp
       bool ok = mbar_wait(x_full, 0, 0x412);
       int si = 0, su = 0;  // first ring: stage of the next tile to wait for, of the step's tile
       uint32_t sp = 0;
@@ -668,66 +668,66 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = ok && (tile = wait_s()) != nullptr;
       if (ok) {
         mma_along(t_s, sm_x, tile);
-        umma_commit(&s_full[0]);
+        umma_commit_warp(&s_full[0]);
         ok = wait_t(0);
       }
       if (is_kv) {
         const uint32_t t_dp = tmem_base + 128, t_dv = tmem_base + 256, t_dk = tmem_base + 384;
         if (ok) {
           mma_along(t_dp, sm_y, sm_t);
-          umma_commit(dp_full);
+          umma_commit_warp(dp_full);
         }
         for (int j = 0; ok && j < n; ++j) {
           const int st = j & 1, nx = (j + 1) & 1;
           if (!mbar_wait(p_ready, j & 1, 0x414)) break;
           tc_fence_after();
           mma_across_bwd(t_dv, t_s, sm_t + st * kAtTile, j > 0);
-          umma_commit(&t_empty[st]);
+          umma_commit_warp(&t_empty[st]);
           if (j + 1 < n) {
             if (!(tile = wait_s())) break;
             mma_along(t_s, sm_x, tile);
-            umma_commit(&s_full[0]);
+            umma_commit_warp(&s_full[0]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x415)) break;
           tc_fence_after();
           mma_across_bwd(t_dk, t_dp, sm_s + su * kAtTile, j > 0);
-          umma_commit(&s_empty[su]);
+          umma_commit_warp(&s_empty[su]);
           if (++su == 3) su = 0;
           if (j + 1 < n) {
             if (!wait_t(j + 1)) break;
             mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
-            umma_commit(dp_full);
+            umma_commit_warp(dp_full);
           }
         }
       } else {
         const uint32_t t_dp = tmem_base + 256, t_dq = tmem_base + 384;
         if (ok) {
           mma_along(t_dp, sm_y, sm_t);
-          umma_commit(dp_full);
-          umma_commit(&t_empty[0]);
+          umma_commit_warp(dp_full);
+          umma_commit_warp(&t_empty[0]);
         }
         for (int j = 0; ok && j < n; ++j) {
           const int nx = (j + 1) & 1;
           if (j + 1 < n) {  // the buffer of S_{j-1}, which dS_{j-1} was made from
             if (!(tile = wait_s())) break;
             mma_along(t_s + nx * 128, sm_x, tile);
-            umma_commit(&s_full[nx]);
+            umma_commit_warp(&s_full[nx]);
           }
           if (!mbar_wait(ds_ready, j & 1, 0x416)) break;
           tc_fence_after();
           mma_across_bwd(t_dq, t_dp, sm_s + su * kAtTile, j > 0);
-          umma_commit(&s_empty[su]);
+          umma_commit_warp(&s_empty[su]);
           if (++su == 3) su = 0;
           if (j + 1 < n) {
             if (!wait_t(j + 1)) break;
             mma_along(t_dp, sm_y, sm_t + nx * kAtTile);
-            umma_commit(dp_full);
-            umma_commit(&t_empty[nx]);
+            umma_commit_warp(dp_full);
+            umma_commit_warp(&t_empty[nx]);
           }
         }
       }
       // every MMA issued here has completed before the results are read and TMEM is freed
-      umma_commit(done);
+      umma_commit_warp(done);
       mbar_wait(done, 0, 0x41a);
     }
   } else {
