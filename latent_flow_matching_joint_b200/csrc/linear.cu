@@ -516,60 +516,67 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         lin_bulk_commit();
       }
     };
-    // 64 columns (half h of the tile half at col0); v: this lane's row; last: no more columns in the matrix.
+    // W columns at a time (the h-th W of the tile half at col0): 32 of fp32
+    // output, whose sums already fill the registers, 64 of bf16. v: this lane's
+    // row; last: no more columns in the matrix.
+    constexpr int W = FINE ? 32 : 64;
     auto finish = [&](float* v, int h, int row0, int col0, bool last) {
-      const int col = col0 + 64 * h;
+      const int col = col0 + W * h;
+      const int odd = FINE ? h & 1 : 0;  // second half of the boxes' 64 fp32 columns
       if (p.slot >= 0) {  // a part's sums, as the boxes are
-        boxes_free();
-        lin_box_write(boxes, lane, v, true, 0);
-        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
-        lin_fence_async();
-        __syncwarp();
-        if (lane == 0) {
-          const int rb = 4 * rank + quarter, cb = 4 * part + 2 * h;
-          lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
-                        boxes, cb + 1 < g.part_cb ? 2 * kLinBox : kLinBox);
-          lin_bulk_commit();
+        if (!odd) boxes_free();
+#pragma unroll
+        for (int q = 0; q < W / 32; ++q) lin_box_write(boxes + (odd + q) * kLinBox, lane, v + 32 * q, true, 0);
+        if (!FINE || odd || last) {
+          lin_fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            const int rb = 4 * rank + quarter, cb = 4 * part + (FINE ? h - odd : 2 * h);
+            lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
+                          boxes, cb + 1 < g.part_cb ? 2 * kLinBox : kLinBox);
+            lin_bulk_commit();
+          }
         }
         return;
       }
       if (!tma) {  // pitches, widths or addresses that TMA cannot take: a column to a lane, row by row
         boxes_free();
-        lin_box_write(boxes, lane, v, true, 0);
-        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
+#pragma unroll
+        for (int q = 0; q < W / 32; ++q) lin_box_write(boxes + q * kLinBox, lane, v + 32 * q, true, 0);
         __syncwarp();
-        lin_finish_column<FINE, FULL>(e, boxes, lane, row0, col + lane);
-        lin_finish_column<FINE, FULL>(e, boxes + kLinBox, lane, row0, col + 32 + lane);
+        for (int q = 0; q < W / 32; ++q)
+          lin_finish_column<FINE, FULL>(e, boxes + q * kLinBox, lane, row0, col + 32 * q + lane);
         __syncwarp();
         return;
       }
       if (has_bias) {
-        const float b0 = col + lane < n ? __ldg(e.bias + col + lane) : 0.f;
-        const float b1 = col + 32 + lane < n ? __ldg(e.bias + col + 32 + lane) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          v[i] += __shfl_sync(0xffffffffu, b0, i);
-          v[32 + i] += __shfl_sync(0xffffffffu, b1, i);
+        for (int q = 0; q < W; q += 32) {
+          const float bias = col + q + lane < n ? __ldg(e.bias + col + q + lane) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[q + i] += __shfl_sync(0xffffffffu, bias, i);
         }
       }
       if (has_z && row0 + lane < m) {  // whole sectors of this lane's row
         __nv_bfloat16* zp = e.z + (row0 + lane) * e.z_ld + col;
 #pragma unroll
-        for (int i = 0; i < 64; i += 8)
+        for (int i = 0; i < W; i += 8)
           if (col + i < n)
             *reinterpret_cast<uint4*>(zp + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
                                                            pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
       }
       if (act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = lin_act(v[i], kActSilu);
+        for (int i = 0; i < W; ++i) v[i] = lin_act(v[i], kActSilu);
       } else if (act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = lin_act(v[i], kActGelu);
+        for (int i = 0; i < W; ++i) v[i] = lin_act(v[i], kActGelu);
       }
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] *= alpha;
-      const bool first = h == 0 || !wide;  // of a round
+      for (int i = 0; i < W; ++i) v[i] *= alpha;
+      // first and last piece of a round: of two in fp32 and if wide, else of itself
+      const bool first = FINE ? !odd : h == 0 || !wide;
+      const bool end = last || (FINE ? odd : !wide);
       if (load_res) {
         if (first) {
           if (!mbar_wait(rbar, res_phase, 0x307)) { ok = false; return; }
@@ -577,35 +584,32 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           res_due = false;
         }
         if (res32) {
-          lin_box_add(boxes, lane, v, true, 0);
-          lin_box_add(boxes + kLinBox, lane, v + 32, true, 0);
+#pragma unroll
+          for (int q = 0; q < W / 32; ++q) lin_box_add(boxes + (odd + q) * kLinBox, lane, v + 32 * q, true, 0);
         } else {
-          uint8_t* box = boxes + (FINE ? 1 : h) * kLinBox;
-          lin_box_add(box, lane, v, false, 0);
-          lin_box_add(box, lane, v + 32, false, 1);
+#pragma unroll
+          for (int q = 0; q < W / 32; ++q)
+            lin_box_add(boxes + (FINE ? 1 : h) * kLinBox, lane, v + 32 * q, false, odd + q);
         }
       } else if (first) {
         boxes_free();
       }
-      if (FINE) {
-        lin_box_write(boxes, lane, v, true, 0);
-        lin_box_write(boxes + kLinBox, lane, v + 32, true, 0);
-      } else {
-        uint8_t* box = boxes + (wide ? h : 0) * kLinBox;
-        lin_box_write(box, lane, v, false, 0);
-        lin_box_write(box, lane, v + 32, false, 1);
-      }
-      if (!wide || last) {
-        store_boxes(wide ? 64 * (h + 1) : 64, row0, wide ? col0 : col);
-        if (load_res && !last && lane == 0) fetch_res(row0, col + 64);
+#pragma unroll
+      for (int q = 0; q < W / 32; ++q)
+        lin_box_write(boxes + (FINE ? odd : (wide ? h : 0)) * kLinBox, lane, v + 32 * q, FINE, q);
+      if (end) {
+        const int before = FINE ? 32 * odd : (wide ? 64 * h : 0);  // columns of the round already in the boxes
+        store_boxes(before + W, row0, col - before);
+        if (load_res && !last && lane == 0) fetch_res(row0, col + W);
       }
     };
     for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
       for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
         const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
         const int col0 = p.ni * 256 + part * 128;
-        const int halves = row0 < m && col0 < n ? (col0 + 64 < n ? 2 : 1) : 0;  // of 64 columns, in the matrix
-        if (load_res && p.slot < 0 && lane == 0 && halves > 0) fetch_res(row0, col0);  // under the main loop
+        int pieces = row0 < m && col0 < n ? (n - col0 + W - 1) / W : 0;  // of W columns, in the matrix
+        if (pieces > 128 / W) pieces = 128 / W;
+        if (load_res && p.slot < 0 && lane == 0 && pieces > 0) fetch_res(row0, col0);  // under the main loop
         if (FINE) {
           const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
           float acc[128];
@@ -629,11 +633,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             release(buf);
           }
 #pragma unroll 1
-          for (int h = 0; ok && h < halves; ++h) {
-            float v[64];
+          for (int h = 0; ok && h < pieces; ++h) {
+            float v[W];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = h ? acc[64 + j] : acc[j];
-            finish(v, h, row0, col0, h == halves - 1);
+            for (int j = 0; j < W; ++j) {
+              const float lo = h & 1 ? acc[(32 + j) & 127] : acc[j], hi = h & 1 ? acc[(96 + j) & 127] : acc[(64 + j) & 127];
+              v[j] = h & 2 ? hi : lo;
+            }
+            finish(v, h, row0, col0, h == pieces - 1);
           }
         } else {
           const int buf = chunk & 1;
@@ -642,13 +649,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tc_fence_after();
           const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-          for (int h = 0; ok && h < halves; ++h) {
+          for (int h = 0; ok && h < pieces; ++h) {
             float v[64];
             tmem_ld64(taddr + 64 * h, v);
-            if (h == halves - 1) release(buf);
-            finish(v, h, row0, col0, h == halves - 1);
+            if (h == pieces - 1) release(buf);
+            finish(v, h, row0, col0, h == pieces - 1);
           }
-          if (halves == 0) release(buf);
+          if (pieces == 0) release(buf);
         }
       }
     }
