@@ -45,7 +45,9 @@ constexpr int kLinStages = 5;
 constexpr int kLinRing = kLinStages * kLinStage;
 constexpr int kLinBox = 4096;                  // 32 rows of 128 bytes: 32 columns of fp32 or 64 of bf16
 constexpr int kLinStaging = 8 * 2 * kLinBox;   // two per epilogue warp
-constexpr int kLinSmem = kLinRing + kLinStaging + 256 + 1024;
+constexpr int kLinBias = 8 * 128;              // 32 columns' bias per epilogue warp
+constexpr int kLinSmem = kLinRing + kLinStaging + kLinBias + 256 + 1024;
+static_assert(kLinSmem <= 227 * 1024, "shared memory of one CTA");
 constexpr int kLinThreads = 384;
 constexpr int kLinChunk = 8;                   // FINE: k blocks (of 64) per TMEM accumulation
 constexpr int kLinSms = 148;                   // the B200's SM count: plans and workspace sizes do not depend on the device
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                        const LinGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLinRing + kLinStaging);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLinRing + kLinStaging + kLinBias);
   uint64_t* empty = full + kLinStages;
   uint64_t* acc_full = empty + kLinStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int part = (warp - 4) >> 2;  // which half of the tile's columns
     const LinEpi& e = g.epi;
     uint8_t* boxes = smem + kLinRing + (warp - 4) * 2 * kLinBox;
+    float* bias_row = reinterpret_cast<float*>(smem + kLinRing + kLinStaging + (warp - 4) * 128);
     uint64_t* rbar = res_full + (warp - 4);
     // What the epilogue asks of its arguments again and again, asked once.
     const bool tma = e.tma, has_bias = FULL && e.bias != nullptr, has_z = FULL && e.z != nullptr;
@@ -516,24 +519,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         lin_bulk_commit();
       }
     };
-    // W columns at a time (the h-th W of the tile half at col0): 32 of fp32
-    // output, whose sums already fill the registers, 64 of bf16. v: this lane's
-    // row; last: no more columns in the matrix.
-    constexpr int W = FINE ? 32 : 64;
+    // 32 columns (the h-th 32 of the tile half at col0); v: this lane's row;
+    // last: no more columns in the matrix.
     auto finish = [&](float* v, int h, int row0, int col0, bool last) {
-      const int col = col0 + W * h;
-      const int odd = FINE ? h & 1 : 0;  // second half of the boxes' 64 fp32 columns
+      const int col = col0 + 32 * h;
+      const int odd = h & 1;
       if (p.slot >= 0) {  // a part's sums, as the boxes are
         if (!odd) boxes_free();
-#pragma unroll
-        for (int q = 0; q < W / 32; ++q) lin_box_write(boxes + (odd + q) * kLinBox, lane, v + 32 * q, true, 0);
-        if (!FINE || odd || last) {
+        lin_box_write(boxes + odd * kLinBox, lane, v, true, 0);
+        if (odd || last) {
           lin_fence_async();
           __syncwarp();
           if (lane == 0) {
-            const int rb = 4 * rank + quarter, cb = 4 * part + (FINE ? h - odd : 2 * h);
+            const int rb = 4 * rank + quarter, cb = 4 * part + h - odd;
             lin_store_raw(g.partial + ((static_cast<long long>(p.slot) * g.part_rb + rb) * g.part_cb + cb) * (kLinBox / 4),
-                          boxes, cb + 1 < g.part_cb ? 2 * kLinBox : kLinBox);
+                          boxes, odd ? 2 * kLinBox : kLinBox);
             lin_bulk_commit();
           }
         }
@@ -541,74 +541,64 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (!tma) {  // pitches, widths or addresses that TMA cannot take: a column to a lane, row by row
         boxes_free();
-#pragma unroll
-        for (int q = 0; q < W / 32; ++q) lin_box_write(boxes + q * kLinBox, lane, v + 32 * q, true, 0);
+        lin_box_write(boxes, lane, v, true, 0);
         __syncwarp();
-        for (int q = 0; q < W / 32; ++q)
-          lin_finish_column<FINE, FULL>(e, boxes + q * kLinBox, lane, row0, col + 32 * q + lane);
-        __syncwarp();
+        lin_finish_column<FINE, FULL>(e, boxes, lane, row0, col + lane);
         return;
       }
       if (has_bias) {
+        __syncwarp();
+        bias_row[lane] = col + lane < n ? __ldg(e.bias + col + lane) : 0.f;
+        __syncwarp();
 #pragma unroll
-        for (int q = 0; q < W; q += 32) {
-          const float bias = col + q + lane < n ? __ldg(e.bias + col + q + lane) : 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[q + i] += __shfl_sync(0xffffffffu, bias, i);
+        for (int i = 0; i < 32; i += 4) {
+          const float4 t = *reinterpret_cast<const float4*>(bias_row + i);
+          v[i] += t.x;
+          v[i + 1] += t.y;
+          v[i + 2] += t.z;
+          v[i + 3] += t.w;
         }
       }
       if (has_z && row0 + lane < m) {  // whole sectors of this lane's row
         __nv_bfloat16* zp = e.z + (row0 + lane) * e.z_ld + col;
 #pragma unroll
-        for (int i = 0; i < W; i += 8)
+        for (int i = 0; i < 32; i += 8)
           if (col + i < n)
             *reinterpret_cast<uint4*>(zp + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
                                                            pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
       }
       if (act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = lin_act(v[i], kActSilu);
+        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActSilu);
       } else if (act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = lin_act(v[i], kActGelu);
+        for (int i = 0; i < 32; ++i) v[i] = lin_act(v[i], kActGelu);
       }
 #pragma unroll
-      for (int i = 0; i < W; ++i) v[i] *= alpha;
-      // first and last piece of a round: of two in fp32 and if wide, else of itself
-      const bool first = FINE ? !odd : h == 0 || !wide;
-      const bool end = last || (FINE ? odd : !wide);
+      for (int i = 0; i < 32; ++i) v[i] *= alpha;
+      const int before = wide ? 32 * h : 32 * odd;  // columns of the round already in the boxes
       if (load_res) {
-        if (first) {
+        if (before == 0) {
           if (!mbar_wait(rbar, res_phase, 0x307)) { ok = false; return; }
           res_phase ^= 1;
           res_due = false;
         }
-        if (res32) {
-#pragma unroll
-          for (int q = 0; q < W / 32; ++q) lin_box_add(boxes + (odd + q) * kLinBox, lane, v + 32 * q, true, 0);
-        } else {
-#pragma unroll
-          for (int q = 0; q < W / 32; ++q)
-            lin_box_add(boxes + (FINE ? 1 : h) * kLinBox, lane, v + 32 * q, false, odd + q);
-        }
-      } else if (first) {
+        lin_box_add(boxes + (res32 ? odd : (FINE ? 1 : h >> 1)) * kLinBox, lane, v, res32, odd);
+      } else if (before == 0) {
         boxes_free();
       }
-#pragma unroll
-      for (int q = 0; q < W / 32; ++q)
-        lin_box_write(boxes + (FINE ? odd : (wide ? h : 0)) * kLinBox, lane, v + 32 * q, FINE, q);
-      if (end) {
-        const int before = FINE ? 32 * odd : (wide ? 64 * h : 0);  // columns of the round already in the boxes
-        store_boxes(before + W, row0, col - before);
-        if (load_res && !last && lane == 0) fetch_res(row0, col + W);
+      lin_box_write(boxes + (FINE ? odd : (wide ? h >> 1 : 0)) * kLinBox, lane, v, FINE, odd);
+      if (last || (!wide && odd)) {
+        store_boxes(before + 32, row0, col - before);
+        if (load_res && !last && lane == 0) fetch_res(row0, col + 32);
       }
     };
     for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
       for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
         const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
         const int col0 = p.ni * 256 + part * 128;
-        int pieces = row0 < m && col0 < n ? (n - col0 + W - 1) / W : 0;  // of W columns, in the matrix
-        if (pieces > 128 / W) pieces = 128 / W;
+        int pieces = row0 < m && col0 < n ? (n - col0 + 31) / 32 : 0;  // of 32 columns, in the matrix
+        if (pieces > 4) pieces = 4;
         if (load_res && p.slot < 0 && lane == 0 && pieces > 0) fetch_res(row0, col0);  // under the main loop
         if (FINE) {
           const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
@@ -634,10 +624,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
 #pragma unroll 1
           for (int h = 0; ok && h < pieces; ++h) {
-            float v[W];
+            float v[32];
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-              const float lo = h & 1 ? acc[(32 + j) & 127] : acc[j], hi = h & 1 ? acc[(96 + j) & 127] : acc[(64 + j) & 127];
+            for (int j = 0; j < 32; ++j) {
+              const float lo = h & 1 ? acc[32 + j] : acc[j], hi = h & 1 ? acc[96 + j] : acc[64 + j];
               v[j] = h & 2 ? hi : lo;
             }
             finish(v, h, row0, col0, h == pieces - 1);
@@ -650,8 +640,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
           for (int h = 0; ok && h < pieces; ++h) {
-            float v[64];
-            tmem_ld64(taddr + 64 * h, v);
+            float v[32];
+            tmem_ld32(taddr + 32 * h, v);
             if (h == pieces - 1) release(buf);
             finish(v, h, row0, col0, h == pieces - 1);
           }
