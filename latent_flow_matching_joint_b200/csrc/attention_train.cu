@@ -803,21 +803,48 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         hand_over(lane_base + 256, ds_ready);
       }
     }
-    if (ok && (n == 0 || mbar_wait(done, 0, 0x41c))) {
+    // The results leave through shared memory (the first ring: everything
+    // loaded into it has been read), so that a warp writes whole rows of 256
+    // bytes. From each lane's own row, 16 bytes in each of 32 rows at a time,
+    // this took 7000 clocks of a dK/dV block's 117000, and takes 2500.
+    const bool finished = ok && (n == 0 || mbar_wait(done, 0, 0x41c));
+    if (finished && n > 0) {
       tc_fence_after();
-      const bool own = rloc < seq.extent(slot);
-      const int row = start + rloc;
-      auto write = [&](const HeadsView& view, uint32_t col, float f) {
-        if (n > 0) tmem_ld_cols<kC>(lane_base + col, d);
-        __nv_bfloat16* dst = head_row(view, b, head, row) + part * kC;
-        if (rloc < valid) store_bf16<kC>(dst, d, f);
-        else if (own) store_zero<kC>(dst);
+      auto stage = [&](int at, uint32_t col, float f) {
+        tmem_ld_cols<kC>(lane_base + col, d);
+        uint8_t* row = sm_s + at * kAtTile + rloc * 256;
+#pragma unroll
+        for (int i = 0; i < kC; i += 8)
+          *reinterpret_cast<uint4*>(row + (((part * kC + i) / 8) ^ (rloc & 7)) * 16) =
+              make_uint4(pack_bf16(d[i] * f, d[i + 1] * f), pack_bf16(d[i + 2] * f, d[i + 3] * f),
+                         pack_bf16(d[i + 4] * f, d[i + 5] * f), pack_bf16(d[i + 6] * f, d[i + 7] * f));
       };
       if (is_kv) {
-        write(a.dv, 256, 1.0f);
-        write(a.dk, 384, a.scale);
+        stage(0, 256, 1.0f);
+        stage(1, 384, a.scale);
       } else {
-        write(a.dq, 384, a.scale);
+        stage(0, 384, a.scale);
+      }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kBwdWarps) : "memory");  // the elementwise warps, finished or not
+    if (finished) {
+      const int extent = seq.extent(slot);
+      const int l = lane & 15;  // 16 bytes of a row
+      auto write = [&](const HeadsView& view, int at) {
+#pragma unroll
+        for (int i = 0; i < 128 / kBwdWarps; i += 2) {
+          const int r = (warp - 2) * (128 / kBwdWarps) + i + (lane >> 4);
+          if (r >= extent) continue;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < valid) v = *reinterpret_cast<const uint4*>(sm_s + at * kAtTile + r * 256 + (l ^ (r & 7)) * 16);
+          *reinterpret_cast<uint4*>(head_row(view, b, head, start + r) + 8 * l) = v;
+        }
+      };
+      if (is_kv) {
+        write(a.dv, 0);
+        write(a.dk, 1);
+      } else {
+        write(a.dq, 0);
       }
     }
   }
