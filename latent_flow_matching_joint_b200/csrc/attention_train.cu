@@ -186,22 +186,6 @@ __device__ __forceinline__ __nv_bfloat16* head_row(const HeadsView& v, int b, in
   return static_cast<__nv_bfloat16*>(v.data) + b * v.batch_stride + head * v.head_stride + row * v.row_stride;
 }
 
-// Stores n (a multiple of 8) floats, times f, as bf16.
-template <int N>
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const float* v, float f) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8)
-    *reinterpret_cast<uint4*>(dst + i) =
-        make_uint4(pack_bf16(v[i] * f, v[i + 1] * f), pack_bf16(v[i + 2] * f, v[i + 3] * f),
-                   pack_bf16(v[i + 4] * f, v[i + 5] * f), pack_bf16(v[i + 6] * f, v[i + 7] * f));
-}
-
-template <int N>
-__device__ __forceinline__ void store_zero(__nv_bfloat16* dst) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
-}
-
 }  // namespace
 
 // Forward. One CTA = two query slots (a, b) of one head, sharing every K/V
@@ -277,7 +261,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int st = j & 1;
         const int slot = seq.used_slot(j), row = seq.start(slot);
-        if (!mbar_wait(&kv_empty[st], ((j >> 1) & 1) ^ 1, 0x401)) break;
+        if (!mbar_wait_warp(&kv_empty[st], ((j >> 1) & 1) ^ 1, 0x401)) break;
         const bool ragged = seq.ragged(slot);
         if (lane == 0) {
           mbar_arrive_expect_tx(&k_full[st], kAtTile);
@@ -289,7 +273,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         if (ragged) {  // V rows that no query may see: P is 0 there, and so must they be
           __syncwarp();
-          if (!mbar_wait(scrub, scrubs & 1, 0x40b)) break;
+          if (!mbar_wait_warp(scrub, scrubs & 1, 0x40b)) break;
           ++scrubs;
           scrub_rows(sm_v + st * kAtTile, seq.valid(slot), lane);
           if (lane == 0) {
@@ -311,7 +295,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         mma_along(tmem_base + t * 256, sm_q + t * kAtTile, sm_k + (j & 1) * kAtTile);
         umma_commit_warp(&s_full[t]);
       };
-      bool ok = mbar_wait(q_full, 0, 0x402) && mbar_wait(&k_full[0], 0, 0x403);
+      bool ok = mbar_wait_warp(q_full, 0, 0x402) && mbar_wait_warp(&k_full[0], 0, 0x403);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0);
@@ -320,9 +304,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const int st = j & 1;
         for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 0 && !mbar_wait(&v_full[st], (j >> 1) & 1, 0x405)) { ok = false; break; }
+          if (t == 0 && !mbar_wait_warp(&v_full[st], (j >> 1) & 1, 0x405)) { ok = false; break; }
           for (int half = 0; half < 2; ++half) {
-            if (!mbar_wait(&p_full[2 * t + half], j & 1, 0x404)) { ok = false; break; }
+            if (!mbar_wait_warp(&p_full[2 * t + half], j & 1, 0x404)) { ok = false; break; }
             tc_fence_after();
             mma_across_half(tmem_base + t * 256 + 128, tmem_base + t * 256 + half * 32, sm_v + st * kAtTile, half,
                             (j | half) != 0);
@@ -331,7 +315,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
           if (t == 1) umma_commit_warp(&kv_empty[st]);
           if (j + 1 < n) {
             if (t == 0) {
-              if (!mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 0x406)) { ok = false; break; }
+              if (!mbar_wait_warp(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, 0x406)) { ok = false; break; }
               tc_fence_after();
             }
             issue_s(t, j + 1);
@@ -342,7 +326,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       }
       // every MMA issued here has completed before TMEM is freed
       umma_commit_warp(drain);
-      mbar_wait(drain, 0, 0x40a);
+      mbar_wait_warp(drain, 0, 0x40a);
     }
   } else {
     const int t = (warp - 2) >> 2;         // query slot of this warpgroup
@@ -358,7 +342,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     float s[128];
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      if (!mbar_wait(&s_full[t], j & 1, 0x407)) { ok = false; break; }
+      if (!mbar_wait_warp(&s_full[t], j & 1, 0x407)) { ok = false; break; }
       tc_fence_after();
       tmem_ld128(s_col, s);
       const int lim = seq.valid(seq.used_slot(j));
@@ -418,16 +402,33 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     const int valid = n > 0 ? seq.valid(slot) : 0;
     const bool own = rloc < seq.extent(slot);
-    if (ok && (n == 0 || mbar_wait(&s_full[t], n & 1, 0x408))) {
+    if (ok && (n == 0 || mbar_wait_warp(&s_full[t], n & 1, 0x408))) {
       tc_fence_after();
+      // The warp's 32 rows leave through shared memory (K's ring: every score
+      // has been made), so that whole rows of 256 bytes are written.
       const float inv = 1.0f / l_run;
-      __nv_bfloat16* dst = head_row(a.out, b, head, row);
-      float o[32];
+      uint8_t* rows32 = sm_k + t * kAtTile + quarter * 32 * 256;
+      if (n > 0) {
+        float o[32];
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        if (n > 0) tmem_ld32(o_col + 32 * c, o);
-        if (rloc < valid) store_bf16<32>(dst + 32 * c, o, inv);
-        else if (own) store_zero<32>(dst + 32 * c);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(o_col + 32 * c, o);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(rows32 + lane * 256 + ((4 * c + i / 8) ^ (lane & 7)) * 16) =
+                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+        }
+        __syncwarp();
+      }
+      const int extent = seq.extent(slot), l = lane & 15;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 2) {
+        const int q = i + (lane >> 4), r = quarter * 32 + q;
+        if (r >= extent) continue;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < valid) v = *reinterpret_cast<const uint4*>(rows32 + q * 256 + (l ^ (q & 7)) * 16);
+        *reinterpret_cast<uint4*>(head_row(a.out, b, head, seq.start(slot) + r) + 8 * l) = v;
       }
       if (own)
         a.lse[(static_cast<long long>(b) * a.heads + head) * a.rows + row] =
@@ -602,14 +603,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t second = kAtTile + (is_kv ? kStatBytes : 0);
         uint64_t* sb = ragged ? scrub : &s_in[ss];
         uint64_t* tb = ragged ? scrub : &t_in[st];
-        if (!mbar_wait(&s_empty[ss], sp ^ 1, 0x411)) break;
+        if (!mbar_wait_warp(&s_empty[ss], sp ^ 1, 0x411)) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(sb, kAtTile + (ragged ? second : 0));
           if (!ragged) slog.armed(ss, sp);
           tile_load(sm_s + ss * kAtTile, ms, sb, row, h, b);
         }
         __syncwarp();
-        if (!mbar_wait(&t_empty[st], tp ^ 1, 0x41d)) break;
+        if (!mbar_wait_warp(&t_empty[st], tp ^ 1, 0x41d)) break;
         if (lane == 0) {
           if (!ragged) {
             mbar_arrive_expect_tx(tb, second);
@@ -619,14 +620,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         __syncwarp();
         if (is_kv) {
-          if (!mbar_wait(&stat_empty[st], tp ^ 1, 0x41e)) break;
+          if (!mbar_wait_warp(&stat_empty[st], tp ^ 1, 0x41e)) break;
           if (lane == 0)
             bulk_load(sm_stat + st * 256, a.stats + ((static_cast<long long>(b) * a.heads + h) * a.slots + from) * 256,
                       kStatBytes, tb);
           __syncwarp();
         }
         if (ragged) {  // rows not in use are summed over by the products: zeros
-          if (!mbar_wait(scrub, scrubs & 1, 0x41b)) break;
+          if (!mbar_wait_warp(scrub, scrubs & 1, 0x41b)) break;
           ++scrubs;
           scrub_rows(sm_s + ss * kAtTile, seq.valid(from), lane);
           scrub_rows(sm_t + st * kAtTile, seq.valid(from), lane);
@@ -648,18 +649,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     if (n > 0) {  // the whole warp, see umma_bf16_warp
-      bool ok = mbar_wait(x_full, 0, 0x412);
+      bool ok = mbar_wait_warp(x_full, 0, 0x412);
       int si = 0, su = 0;  // first ring: stage of the next tile to wait for, of the step's tile
       uint32_t sp = 0;
       auto wait_s = [&]() -> const uint8_t* {  // the next first tile, or null
-        if (!mbar_wait(&s_in[si], sp, 0x413)) return nullptr;
+        if (!mbar_wait_warp(&s_in[si], sp, 0x413)) return nullptr;
         tc_fence_after();
         const uint8_t* tile = sm_s + si * kAtTile;
         if (++si == 3) { si = 0; sp ^= 1; }
         return tile;
       };
       auto wait_t = [&](int j) {
-        const bool r = mbar_wait(&t_in[j & 1], (j >> 1) & 1, 0x413);
+        const bool r = mbar_wait_warp(&t_in[j & 1], (j >> 1) & 1, 0x413);
         if (r) tc_fence_after();
         return r;
       };
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         for (int j = 0; ok && j < n; ++j) {
           const int st = j & 1, nx = (j + 1) & 1;
-          if (!mbar_wait(p_ready, j & 1, 0x414)) break;
+          if (!mbar_wait_warp(p_ready, j & 1, 0x414)) break;
           tc_fence_after();
           mma_across_bwd(t_dv, t_s, sm_t + st * kAtTile, j > 0);
           umma_commit_warp(&t_empty[st]);
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mma_along(t_s, sm_x, tile);
             umma_commit_warp(&s_full[0]);
           }
-          if (!mbar_wait(ds_ready, j & 1, 0x415)) break;
+          if (!mbar_wait_warp(ds_ready, j & 1, 0x415)) break;
           tc_fence_after();
           mma_across_bwd(t_dk, t_dp, sm_s + su * kAtTile, j > 0);
           umma_commit_warp(&s_empty[su]);
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mma_along(t_s + nx * 128, sm_x, tile);
             umma_commit_warp(&s_full[nx]);
           }
-          if (!mbar_wait(ds_ready, j & 1, 0x416)) break;
+          if (!mbar_wait_warp(ds_ready, j & 1, 0x416)) break;
           tc_fence_after();
           mma_across_bwd(t_dq, t_dp, sm_s + su * kAtTile, j > 0);
           umma_commit_warp(&s_empty[su]);
@@ -728,7 +729,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       // every MMA issued here has completed before the results are read and TMEM is freed
       umma_commit_warp(done);
-      mbar_wait(done, 0, 0x41a);
+      mbar_wait_warp(done, 0, 0x41a);
     }
   } else {
     constexpr int kC = kBwdCols;
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // the statistics come with the second streamed tile
         const float4* lse = reinterpret_cast<const float4*>(sm_stat + (j & 1) * 256 + part * kC);
         const float4* dd = lse + 32;
-        if (!mbar_wait(&t_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait(&s_full[0], j & 1, 0x417)) { ok = false; break; }
+        if (!mbar_wait_warp(&t_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait_warp(&s_full[0], j & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base, p);
 #pragma unroll
@@ -765,7 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           pk[(i >> 1) + 1] = pack_bf16(p[i + 2], p[i + 3]);
         }
         hand_over(lane_base, p_ready);
-        if (!mbar_wait(dp_full, j & 1, 0x418)) { ok = false; break; }
+        if (!mbar_wait_warp(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base + 128, d);
 #pragma unroll
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
       const float lse = stat[rloc], dd = stat[128 + rloc];
       for (int j = 0; j < n; ++j) {
-        if (!mbar_wait(&s_full[j & 1], (j >> 1) & 1, 0x417)) { ok = false; break; }
+        if (!mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base + (j & 1) * 128, p);
 #pragma unroll
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int i = 0; i < kC; ++i) p[i] = i < lim ? p[i] : 0.f;
         }
-        if (!mbar_wait(dp_full, j & 1, 0x418)) { ok = false; break; }
+        if (!mbar_wait_warp(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
         tmem_ld_cols<kC>(lane_base + 256, d);
 #pragma unroll
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // loaded into it has been read), so that a warp writes whole rows of 256
     // bytes. From each lane's own row, 16 bytes in each of 32 rows at a time,
     // this took 7000 clocks of a dK/dV block's 117000, and takes 2500.
-    const bool finished = ok && (n == 0 || mbar_wait(done, 0, 0x41c));
+    const bool finished = ok && (n == 0 || mbar_wait_warp(done, 0, 0x41c));
     if (finished && n > 0) {
       tc_fence_after();
       auto stage = [&](int at, uint32_t col, float f) {

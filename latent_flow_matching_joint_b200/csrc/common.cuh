@@ -174,6 +174,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
   }
 }
 
+// The same for a whole converged warp, all lanes with the same answer: on what
+// follows, warp-wide instructions rely on every lane being there.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, site));
+}
+
 // Stages of a TMA ring whose full barrier this thread armed, and the phase
 // of each last arming. drain() waits (bounded) for those phases, so that a
 // producer that stops early (a wait gave up) leaves no TMA write in flight

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int before = wide ? 32 * h : 32 * odd;  // columns of the round already in the boxes
       if (load_res) {
         if (before == 0) {
-          if (!mbar_wait(rbar, res_phase, 0x307)) { ok = false; return; }
+          if (!mbar_wait_warp(rbar, res_phase, 0x307)) { ok = false; return; }
           res_phase ^= 1;
           res_due = false;
         }
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           float acc[128];
           for (int c = 0; c < chunks; ++c, ++chunk) {
             const int buf = chunk & 1;
-            if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
+            if (!mbar_wait_warp(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
             tc_fence_after();
             const uint32_t taddr =
                 tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         } else {
           const int buf = chunk & 1;
-          if (!mbar_wait(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
+          if (!mbar_wait_warp(&acc_full[buf], (chunk >> 1) & 1, 0x304)) { ok = false; break; }
           ++chunk;
           tc_fence_after();
           const uint32_t taddr = tmem_base + buf * 256 + part * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
