@@ -433,7 +433,7 @@ typedef struct {
  * query head h reads key head h / (heads / kv_heads), heads a multiple of
  * kv_heads. scale > 0 multiplies q . k (1 / sqrt(128) in the denoiser).
  * txt_len: NULL, then every row attends to every row, as in the denoiser
- * (n_txt is not looked at); or device int [batch], the number of text tokens of
+ * (n_txt only has to lie in [0, rows]); or device int [batch], the number of text tokens of
  * each item (clamped to [0, n_txt]): its rows [txt_len, n_txt) are padding.
  * Padding neither attends nor is attended to, whatever its rows hold (NaN
  * included): their out and gradients are 0, their lse -infinity. */

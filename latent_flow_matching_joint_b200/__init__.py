@@ -471,6 +471,7 @@ def klein_op_time_mod(model: KleinModel, sigma: float, sigma_next: float, with_r
 # device raises KleinError and nothing is enqueued. The work goes to the
 # tensors' device, on its current stream unless `stream` names another.
 
+INT_MAX = 2 ** 31 - 1  # sizes are C ints: a larger one would arrive as another number
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 
 
@@ -531,6 +532,8 @@ def _attention_shape(q, k, n_txt, txt_len, scale):
     kv_heads = k.shape[1]
     if d != HEAD_DIM:
         _refuse(-2, f"q has heads of {d}, not {HEAD_DIM}")
+    if max(batch, heads, rows, kv_heads) > INT_MAX or not 0 <= n_txt <= rows:
+        _refuse(-2, "q or k too large, or n_txt outside [0, rows]")
     if txt_len is not None:
         _vector("txt_len", txt_len, batch, _torch.int32)
         txt_len = txt_len.data_ptr()
@@ -561,6 +564,8 @@ def klein_op_attention_forward(q, k, v, out, lse, n_txt: int = 0, txt_len=None, 
 
 
 def klein_attention_backward_workspace_size(batch: int, heads: int, rows: int, n_txt: int = 0) -> int:
+    if max(batch, heads, rows, n_txt) > INT_MAX:
+        return 0
     return lib.klein_attention_backward_workspace_size(batch, heads, rows, n_txt)
 
 
@@ -617,11 +622,14 @@ def _linear_sizes(x, w, act):
     if act not in ACTIVATIONS:
         _refuse(-1, f"unknown activation {act!r}")
     m, k = x.shape
-    return m, w.shape[0], k, ACTIVATIONS[act]
+    n = w.shape[0]
+    if m > INT_MAX or n > INT_MAX or k > INT_MAX:
+        _refuse(-2, "matrix too large")
+    return m, n, k, ACTIVATIONS[act]
 
 
 def klein_linear_workspace_size(m: int, n: int, k: int) -> int:
-    return lib.klein_linear_workspace_size(m, n, k)
+    return lib.klein_linear_workspace_size(m, n, k) if max(m, n, k) <= INT_MAX else 0
 
 
 def klein_op_linear(x, w, out, ws=None, bias=None, residual=None, act: str = "none", alpha: float = 1.0,
@@ -645,7 +653,7 @@ def klein_op_linear(x, w, out, ws=None, bias=None, residual=None, act: str = "no
 
 
 def klein_linear_backward_workspace_size(m: int, n: int, k: int) -> int:
-    return lib.klein_linear_backward_workspace_size(m, n, k)
+    return lib.klein_linear_backward_workspace_size(m, n, k) if max(m, n, k) <= INT_MAX else 0
 
 
 def klein_op_linear_backward(dout, x, w, ws, dx=None, dw=None, dbias=None, preact=None, act: str = "none",

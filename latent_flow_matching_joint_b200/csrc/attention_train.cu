@@ -113,7 +113,7 @@ struct Slots {
     slots = a.slots;
     len = 0;
     if (a.txt_len) {
-      len = __ldg(a.txt_len + b);
+      len = a.txt_len[b];  // (a plain load: the kernel before this one may have written it, see pdl_wait)
       len = len < 0 ? 0 : (len > n_txt ? n_txt : len);
     }
   }

@@ -156,10 +156,10 @@ __device__ __forceinline__ void lin_finish4(const LinEpi& e, long long row, int 
 __device__ __forceinline__ float4 lin_bias4(const LinEpi& e, int col) {
   float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
   if (e.bias) {
-    if (col + 0 < e.n) b.x = __ldg(e.bias + col);
-    if (col + 1 < e.n) b.y = __ldg(e.bias + col + 1);
-    if (col + 2 < e.n) b.z = __ldg(e.bias + col + 2);
-    if (col + 3 < e.n) b.w = __ldg(e.bias + col + 3);
+    if (col + 0 < e.n) b.x = e.bias[col];
+    if (col + 1 < e.n) b.y = e.bias[col + 1];
+    if (col + 2 < e.n) b.z = e.bias[col + 2];
+    if (col + 3 < e.n) b.w = e.bias[col + 3];
   }
   return b;
 }
@@ -275,7 +275,7 @@ template <bool OUT32, bool FULL>
 __device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t* box, int lane, int row0, int col) {
   const int rows = e.m - row0 < 32 ? e.m - row0 : 32;
   if (col >= e.n) return;
-  const float bias = FULL && e.bias ? __ldg(e.bias + col) : 0.f;
+  const float bias = FULL && e.bias ? e.bias[col] : 0.f;
   const long long out_ld = e.out_ld, res_ld = e.res_ld, z_ld = e.z_ld;
   float* o32 = static_cast<float*>(e.out) + row0 * out_ld + col;
   __nv_bfloat16* o16 = static_cast<__nv_bfloat16*>(e.out) + row0 * out_ld + col;
@@ -386,87 +386,90 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
   LinPiece p;
 
+  // Loads here and below are plain ones, not __ldg: this kernel may start while
+  // the one that writes an operand still runs (programmatic dependent launch),
+  // and only plain loads see its writes after pdl_wait.
   if (warp < 4) {
     if (FINE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      StageLog log;
-      bool ok = true;
-      for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
-        for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
-          const int row = p.mi * 256 + 128 * rank, col = p.ni * 256 + 128 * rank;
-          for (int kb = p.kb0; kb < p.kb1; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1, 0x301)) { ok = false; break; }
-            if (leader) {
-              mbar_arrive_expect_tx(&full[stage], 2 * kLinStage);
-              log.armed(stage, phase);
-            }
-            uint8_t* sa = smem + stage * kLinStage;
-            uint8_t* sb = sa + kLinTile;
-            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-            // the second pass over k reads A's low halves against the same B
-            const int kb_b = kb >= g.k_wrap ? kb - g.k_wrap : kb;
-            if (AMN) {
-              const int r = kb >= g.k_wrap ? row + g.a_low : row;
-              tma_load_2d_pair(sa, &map_a, bar, r, kb_b * 64);
-              tma_load_2d_pair(sa + kLinTile / 2, &map_a, bar, r + 64, kb_b * 64);
-            } else {
-              tma_load_2d_pair(sa, &map_a, bar, kb >= g.k_wrap ? kb_b * 64 + g.a_low : kb * 64, row);
-            }
-            if (BMN) {
-              tma_load_2d_pair(sb, &map_b, bar, col, kb_b * 64);
-              tma_load_2d_pair(sb + kLinTile / 2, &map_b, bar, col + 64, kb_b * 64);
-            } else {
-              tma_load_2d_pair(sb, &map_b, bar, kb_b * 64, col);
-            }
-            if (++stage == kLinStages) { stage = 0; phase ^= 1; }
-          }
-        }
-      }
-      // No TMA write of the pair may land after it exits: the leader's
-      // barriers count both CTAs' bytes, and the cluster barrier below keeps
-      // the other CTA alive.
-      if (leader) log.drain(full, kLinStages, 0x305);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int chunk = 0;
-      bool ok = true;
-      for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
-        for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
-          for (int kb = p.kb0; ok && kb < p.kb1; ++chunk) {
-            const int acc = chunk & 1;
-            if (!mbar_wait(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, 0x302)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t d = tmem_base + acc * 256;
-            const int first = kb;
-            const int end = FINE && kb + kLinChunk < p.kb1 ? kb + kLinChunk : p.kb1;
-            for (; kb < end; ++kb) {
-              if (!mbar_wait(&full[stage], phase, 0x303)) { ok = false; break; }
-              tc_fence_after();
-              const uint32_t a0 = smem_u32(smem + stage * kLinStage);
-              const uint32_t b0 = a0 + kLinTile;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint64_t da = AMN ? sw128_desc_mn(a0 + 2048 * k, kLinTile / 2) : sw128_desc(a0 + 32 * k);
-                const uint64_t db = BMN ? sw128_desc_mn(b0 + 2048 * k, kLinTile / 2) : sw128_desc(b0 + 32 * k);
-                umma_bf16_pair(d, da, db, idesc, kb != first || k != 0);
+    if (warp == 0) {
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        StageLog log;
+        bool ok = true;
+        for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
+          for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
+            const int row = p.mi * 256 + 128 * rank, col = p.ni * 256 + 128 * rank;
+            for (int kb = p.kb0; kb < p.kb1; ++kb) {
+              if (!mbar_wait(&empty[stage], phase ^ 1, 0x301)) { ok = false; break; }
+              if (leader) {
+                mbar_arrive_expect_tx(&full[stage], 2 * kLinStage);
+                log.armed(stage, phase);
               }
-              umma_commit_pair(&empty[stage], 0x3);
+              uint8_t* sa = smem + stage * kLinStage;
+              uint8_t* sb = sa + kLinTile;
+              const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+              // the second pass over k reads A's low halves against the same B
+              const int kb_b = kb >= g.k_wrap ? kb - g.k_wrap : kb;
+              if (AMN) {
+                const int r = kb >= g.k_wrap ? row + g.a_low : row;
+                tma_load_2d_pair(sa, &map_a, bar, r, kb_b * 64);
+                tma_load_2d_pair(sa + kLinTile / 2, &map_a, bar, r + 64, kb_b * 64);
+              } else {
+                tma_load_2d_pair(sa, &map_a, bar, kb >= g.k_wrap ? kb_b * 64 + g.a_low : kb * 64, row);
+              }
+              if (BMN) {
+                tma_load_2d_pair(sb, &map_b, bar, col, kb_b * 64);
+                tma_load_2d_pair(sb + kLinTile / 2, &map_b, bar, col + 64, kb_b * 64);
+              } else {
+                tma_load_2d_pair(sb, &map_b, bar, kb_b * 64, col);
+              }
               if (++stage == kLinStages) { stage = 0; phase ^= 1; }
             }
-            if (ok) umma_commit_pair(&acc_full[acc], 0x3);
           }
         }
+        // No TMA write of the pair may land after it exits: the leader's
+        // barriers count both CTAs' bytes, and the cluster barrier below keeps
+        // the other CTA alive.
+        if (leader) log.drain(full, kLinStages, 0x305);
       }
-      // every MMA issued here has completed before TMEM is freed
-      umma_commit_pair(drain, 0x1);
-      mbar_wait(drain, 0, 0x306);
-    }
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int chunk = 0;
+        bool ok = true;
+        for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
+          for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
+            for (int kb = p.kb0; ok && kb < p.kb1; ++chunk) {
+              const int acc = chunk & 1;
+              if (!mbar_wait(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, 0x302)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t d = tmem_base + acc * 256;
+              const int first = kb;
+              const int end = FINE && kb + kLinChunk < p.kb1 ? kb + kLinChunk : p.kb1;
+              for (; kb < end; ++kb) {
+                if (!mbar_wait(&full[stage], phase, 0x303)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t a0 = smem_u32(smem + stage * kLinStage);
+                const uint32_t b0 = a0 + kLinTile;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint64_t da = AMN ? sw128_desc_mn(a0 + 2048 * k, kLinTile / 2) : sw128_desc(a0 + 32 * k);
+                  const uint64_t db = BMN ? sw128_desc_mn(b0 + 2048 * k, kLinTile / 2) : sw128_desc(b0 + 32 * k);
+                  umma_bf16_pair(d, da, db, idesc, kb != first || k != 0);
+                }
+                umma_commit_pair(&empty[stage], 0x3);
+                if (++stage == kLinStages) { stage = 0; phase ^= 1; }
+              }
+              if (ok) umma_commit_pair(&acc_full[acc], 0x3);
+            }
+          }
+        }
+        // every MMA issued here has completed before TMEM is freed
+        umma_commit_pair(drain, 0x1);
+        mbar_wait(drain, 0, 0x306);
+      }
     }
   } else {
     if (FINE) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (has_bias) {
         __syncwarp();
-        bias_row[lane] = col + lane < n ? __ldg(e.bias + col + lane) : 0.f;
+        bias_row[lane] = col + lane < n ? e.bias[col + lane] : 0.f;
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
@@ -695,12 +698,12 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinGemmArgs g)
 
 // Eight bf16 of a row from column k on, zeros past the row's end.
 __device__ __forceinline__ uint4 lin_load8(const __nv_bfloat16* row, int k, int k_end) {
-  if (k + 8 <= k_end) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (k + 8 <= k_end) return *reinterpret_cast<const uint4*>(row + k);
   uint32_t u[4] = {0u, 0u, 0u, 0u};
   const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (k + i < k_end) u[i >> 1] |= static_cast<uint32_t>(__ldg(r + k + i)) << (16 * (i & 1));
+    if (k + i < k_end) u[i >> 1] |= static_cast<uint32_t>(r[k + i]) << (16 * (i & 1));
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
@@ -762,13 +765,13 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const __nv_bflo
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int at = k0 + 32 * u + 8 * t;
-        a[u] = __ldg(reinterpret_cast<const uint4*>(w0 + at));
-        a8[u] = __ldg(reinterpret_cast<const uint4*>(w1 + at));
+        a[u] = __ldcs(reinterpret_cast<const uint4*>(w0 + at));
+        a8[u] = __ldcs(reinterpret_cast<const uint4*>(w1 + at));
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) xv[u][b] = __ldg(reinterpret_cast<const uint4*>(xr[b] + k0 + 32 * u + 8 * t));
+        for (int b = 0; b < NB; ++b) xv[u][b] = *reinterpret_cast<const uint4*>(xr[b] + k0 + 32 * u + 8 * t);
 #pragma unroll
       for (int u = 0; u < 4; ++u) step(a[u], a8[u], xv[u]);
     } else {
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(32 * WARPS) linear_rows_kernel(const __nv_bflo
 #pragma unroll
     for (int q = 1; q < WARPS; ++q) v += part[q][r][i & 15];
     const long long row = row0 + r;
-    const float z = v + (e.bias ? __ldg(e.bias + col) : 0.f);
+    const float z = v + (e.bias ? e.bias[col] : 0.f);
     const float res = e.res ? lin_load(e.res, row * e.res_ld + col, e.res_f32) : 0.f;
     if (e.z) e.z[row * e.z_ld + col] = __float2bfloat16_rn(z);
     const float y = fmaf(e.alpha, lin_act(z, e.act), res);
@@ -859,8 +862,8 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(const LinDzArgs a) {
     }
   };
   if (count == 8 && a.dout_vec && !a.dout_f32 && (ACT == kActNone || a.z_vec)) {
-    // Four rows' loads in flight per warp and all the registers that takes: 4608 x 9216 with GELU in 57 us (255 MB,
-    // floor 39); two rows 61, one row 56 without and 70 with a higher occupancy, one row in the general form 94.
+    // Four rows' loads in flight per warp and the registers that takes (two blocks per SM): 4608 x 9216 with GELU in
+    // about 57 us (255 MB, floor 39). Three blocks per SM spill: 94; two rows and four blocks 60; one row and six 84.
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(a.dout) + col;
     const __nv_bfloat16* zp = a.z + col;
     for (long long r = r0 + warp; r < r1; r += 32) {
