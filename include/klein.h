@@ -27,8 +27,9 @@
  *     gave up (no progress for the wait limit) is recorded on the device and
  *     reported by klein_sync(stream) or klein_device_status() as
  *     KLEIN_ERR_TIMEOUT.
- *   - Device pointers must be 16-byte aligned. The model width is fixed at
- *     KLEIN_DIM = 3072, 24 heads of 128.
+ *   - Device pointers must be 16-byte aligned, unless a call states less. The
+ *     model width is fixed at KLEIN_DIM = 3072, 24 heads of 128 (the training
+ *     ops take any width and head count).
  *   - bf16 = IEEE bfloat16 stored as uint16; all matrices are row-major.
  *   - Nothing is thrown across the ABI; no call allocates device memory:
  *     scratch comes from the caller's workspace.

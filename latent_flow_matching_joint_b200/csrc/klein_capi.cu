@@ -473,7 +473,7 @@ extern "C" {
 
 const char* klein_last_error(void) { return g_msg; }
 
-int klein_version(void) { return 103; }
+int klein_version(void) { return 104; }
 
 long long klein_launch_count(void) { return g_launches; }
 
