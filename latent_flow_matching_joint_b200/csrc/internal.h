@@ -174,7 +174,6 @@ struct LinGemmArgs {
   int waves, whole;    // the first `whole` tiles are dealt out whole, in `waves` rounds
   int pairs;           // CTA pairs that the work is dealt out to
   int cut, parts;      // the last `cut` tiles are cut along k into `parts` equal parts each
-  int deep;            // short k with a bf16 residual: see kLinDeepStages
   int n_fastest;       // number the tiles N-fastest instead of M-fastest
   float* partial;      // [parts][cut][part_rb][part_cb] boxes of 32 x 32, the parts' sums
   int part_rb, part_cb;

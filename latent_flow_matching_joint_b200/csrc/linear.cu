@@ -44,12 +44,7 @@ constexpr int kLinStage = 2 * kLinTile;        // A and B
 constexpr int kLinStages = 5;
 constexpr int kLinRing = kLinStages * kLinStage;
 constexpr int kLinBox = 4096;                  // 32 rows of 128 bytes: 32 columns of fp32 or 64 of bf16
-constexpr int kLinStaging = 8 * 2 * kLinBox;   // a pair of boxes per epilogue warp
-// Short k, bf16 and a residual: the output is all the work, and the ring needs
-// only 3 stages. The other two become a second pair of boxes per warp, into which
-// the next tile's residual comes while this one is finished.
-constexpr int kLinDeepStages = 3;
-static_assert((kLinStages - kLinDeepStages) * kLinStage == kLinStaging, "the second boxes fill the stages left over");
+constexpr int kLinStaging = 8 * 2 * kLinBox;   // two per epilogue warp
 constexpr int kLinBias = 8 * 128;              // 32 columns' bias per epilogue warp
 constexpr int kLinSmem = kLinRing + kLinStaging + kLinBias + 256 + 1024;
 static_assert(kLinSmem <= 227 * 1024, "shared memory of one CTA");
@@ -349,8 +344,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint64_t* acc_full = empty + kLinStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint64_t* res_full = drain + 1;  // [8 epilogue warps][2 pairs of boxes]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 16);
+  uint64_t* res_full = drain + 1;  // [8 epilogue warps]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 8);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -367,7 +362,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(&acc_empty[a], 16);  // one arrival per epilogue warp of the pair
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < 16; ++i) mbar_init(&res_full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&res_full[i], 1);
     fence_barrier_init();
     tma_prefetch_desc(&map_a);
     tma_prefetch_desc(&map_b);
@@ -388,7 +383,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   pdl_wait();  // operands and outputs are touched only after the previous kernel completes
 
   const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int stages = !FINE && g.deep ? kLinDeepStages : kLinStages;
   constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
   LinPiece p;
 
@@ -430,14 +424,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               } else {
                 tma_load_2d_pair(sb, &map_b, bar, kb_b * 64, col);
               }
-              if (++stage == stages) { stage = 0; phase ^= 1; }
+              if (++stage == kLinStages) { stage = 0; phase ^= 1; }
             }
           }
         }
         // No TMA write of the pair may land after it exits: the leader's
         // barriers count both CTAs' bytes, and the cluster barrier below keeps
         // the other CTA alive.
-        if (leader) log.drain(full, stages, 0x305);
+        if (leader) log.drain(full, kLinStages, 0x305);
       }
     } else if (warp == 1) {
       if (lane == 0 && leader) {
@@ -466,7 +460,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                   umma_bf16_pair(d, da, db, idesc, kb != first || k != 0);
                 }
                 umma_commit_pair(&empty[stage], 0x3);
-                if (++stage == stages) { stage = 0; phase ^= 1; }
+                if (++stage == kLinStages) { stage = 0; phase ^= 1; }
               }
               if (ok) umma_commit_pair(&acc_full[acc], 0x3);
             }
@@ -482,13 +476,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int quarter = warp & 3;
     const int part = (warp - 4) >> 2;  // which half of the tile's columns
     const LinEpi& e = g.epi;
-    const bool deep = !FINE && g.deep;
-    uint8_t* const first_boxes = smem + kLinRing + (warp - 4) * 2 * kLinBox;
-    uint8_t* const second_boxes = smem + kLinDeepStages * kLinStage + (warp - 4) * 2 * kLinBox;  // deep
-    uint8_t* boxes = first_boxes;
-    int set = 0;
+    uint8_t* boxes = smem + kLinRing + (warp - 4) * 2 * kLinBox;
     float* bias_row = reinterpret_cast<float*>(smem + kLinRing + kLinStaging + (warp - 4) * 128);
-    uint64_t* rbar = res_full + 2 * (warp - 4);
+    uint64_t* rbar = res_full + (warp - 4);
     // What the epilogue asks of its arguments again and again, asked once.
     const bool tma = e.tma, has_bias = FULL && e.bias != nullptr, has_z = FULL && e.z != nullptr;
     const bool load_res = tma && e.res, res32 = e.res_f32;
@@ -497,8 +487,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int m = e.m, n = e.n;
     // A round is what the two boxes hold: 128 columns if everything is bf16, else 64.
     const bool wide = !FINE && !(load_res && res32);
-    uint32_t res_phase = 0;  // bit s: parity of the next residual for the s-th boxes
-    uint32_t res_due = 0;    // lane 0, bit s: a residual is on its way to them
+    uint32_t res_phase = 0;  // parity of the next residual
+    bool res_due = false;    // lane 0: a residual is on its way
     int chunk = 0;
     bool ok = true;
     auto release = [&](int buf) {
@@ -506,16 +496,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_tmem(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     };
-    auto fetch_res = [&](int to, int row0, int col) {  // lane 0: a round's residual, into boxes that nothing uses
+    auto fetch_res = [&](int row0, int col) {  // lane 0: a round's residual, into boxes that nothing uses
       lin_bulk_wait_read();
-      uint8_t* dst = to ? second_boxes : first_boxes;
       const int per_box = res32 ? 32 : 64;
       const bool two = (wide || res32) && col + per_box < n;
-      mbar_arrive_expect_tx(&rbar[to], two ? 2 * kLinBox : kLinBox);
-      res_due |= 1u << to;
+      mbar_arrive_expect_tx(rbar, two ? 2 * kLinBox : kLinBox);
+      res_due = true;
       // (64 columns of bf16 lie in the second box if the output is fp32: the lane reads them all before it writes)
-      tma_load_2d(dst + (FINE && !res32 ? kLinBox : 0), &map_res, &rbar[to], col, row0);
-      if (two) tma_load_2d(dst + kLinBox, &map_res, &rbar[to], col + per_box, row0);
+      tma_load_2d(boxes + (FINE && !res32 ? kLinBox : 0), &map_res, rbar, col, row0);
+      if (two) tma_load_2d(boxes + kLinBox, &map_res, rbar, col + per_box, row0);
     };
     auto boxes_free = [&]() {
       if (lane == 0) lin_bulk_wait_read();
@@ -592,9 +581,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int before = wide ? 32 * h : 32 * odd;  // columns of the round already in the boxes
       if (load_res) {
         if (before == 0) {
-          if (!mbar_wait_warp(&rbar[set], (res_phase >> set) & 1, 0x307)) { ok = false; return; }
-          res_phase ^= 1u << set;
-          res_due &= ~(1u << set);
+          if (!mbar_wait_warp(rbar, res_phase, 0x307)) { ok = false; return; }
+          res_phase ^= 1;
+          res_due = false;
         }
         lin_box_add(boxes + (res32 ? odd : (FINE ? 1 : h >> 1)) * kLinBox, lane, v, res32, odd);
       } else if (before == 0) {
@@ -603,31 +592,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       lin_box_write(boxes + (FINE ? odd : (wide ? h >> 1 : 0)) * kLinBox, lane, v, FINE, odd);
       if (last || (!wide && odd)) {
         store_boxes(before + 32, row0, col - before);
-        if (load_res && !last && lane == 0) fetch_res(0, row0, col + 32);  // (never so if deep: one round)
+        if (load_res && !last && lane == 0) fetch_res(row0, col + 32);
       }
-    };
-    // This warp's part of a piece: its first row and column, and how many 32 columns of it are in the matrix.
-    struct Place {
-      int row0, col0, pieces;
-    };
-    auto place = [&](const LinPiece& q) {
-      const int row0 = q.mi * 256 + 128 * rank + quarter * 32, col0 = q.ni * 256 + part * 128;
-      int pieces = row0 < m && col0 < n ? (n - col0 + 31) / 32 : 0;
-      return Place{row0, col0, pieces > 4 ? 4 : pieces};
     };
     for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
       for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
-        const Place at = place(p);
-        const int row0 = at.row0, col0 = at.col0, pieces = at.pieces;
-        if (load_res && lane == 0) {  // under the main loop, or the tile before
-          if ((!deep || i == 0) && p.slot < 0 && pieces > 0) fetch_res(set, row0, col0);
-          LinPiece next;
-          if (deep && lin_piece(g, pair, i + 1, next)) {
-            const Place then = place(next);
-            if (then.pieces > 0) fetch_res(set ^ 1, then.row0, then.col0);
-          }
-        }
-        boxes = set ? second_boxes : first_boxes;
+        const int row0 = p.mi * 256 + 128 * rank + quarter * 32;
+        const int col0 = p.ni * 256 + part * 128;
+        int pieces = row0 < m && col0 < n ? (n - col0 + 31) / 32 : 0;  // of 32 columns, in the matrix
+        if (pieces > 4) pieces = 4;
+        if (load_res && p.slot < 0 && lane == 0 && pieces > 0) fetch_res(row0, col0);  // under the main loop
         if (FINE) {
           const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
           float acc[128];
@@ -675,15 +649,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
           if (pieces == 0) release(buf);
         }
-        if (deep) set ^= 1;
       }
     }
     if (lane == 0) {
       // when the CTA exits no store may still read shared memory, and (after a
       // wait that gave up) no residual may still be on its way
       lin_bulk_wait_all();
-      for (int b = 0; b < 2; ++b)
-        if ((res_due >> b) & 1u) mbar_wait(&rbar[b], (res_phase >> b) & 1, 0x308);
+      if (res_due) mbar_wait(rbar, res_phase, 0x308);
     }
   }
 
@@ -1065,7 +1037,6 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
   if (g.epi.tma && (make_map_rows32(&mo, epi.out, epi.n, epi.m, epi.out_ld, epi.out_f32) ||
                     (epi.res && make_map_rows32(&mr, epi.res, epi.n, epi.m, epi.res_ld, epi.res_f32))))
     return -2;
-  g.deep = g.epi.tma && epi.res && !epi.res_f32 && !epi.out_f32 && g.k_blocks <= kLinDeepStages;
   int rc;
   const bool fine = epi.out_f32, full = epi.bias || epi.z || epi.act != kActNone;
   if (a.mn_major) {

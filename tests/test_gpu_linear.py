@@ -112,6 +112,16 @@ def test_linear_epilogues(kb, act, residual, out, m, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k", [8, 16, 64, 65, 192, 193, 256])
+@pytest.mark.parametrize("m,n", [(5000, 5000), (700, 9000), (20000, 264), (9000, 1032)])
+def test_linear_short_k_with_residual(kb, m, n, k):
+    """An adapter's second half over many tiles, onto the frozen layer's output."""
+    for in_place in (False, True):
+        check_forward(kb, m, n, k, residual=torch.bfloat16, alpha=2.0, in_place=in_place)
+    check_forward(kb, m, n, k, act="silu", bias=True, residual=torch.bfloat16, save=True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m,n,k", [(2, 100, 3000), (64, 100, 12288), (300, 700, 9216), (2000, 3000, 4096)])
 def test_linear_long_sums_keep_fp32(kb, m, n, k):
     """fp32 output of long sums: the norm of the error is that of fp32 sums, not of a truncating accumulator
