@@ -270,8 +270,9 @@ __device__ __forceinline__ void lin_fence_async() { asm volatile("fence.proxy.as
 
 // The epilogue element by element: this lane's column of a box of fp32 sums,
 // 32 rows from row0 on. Any pitch, width and alignment; a row's 32 elements
-// are one access of the warp. Eight rows' residuals are in flight at a time.
-template <bool OUT32, bool FULL>
+// are one access of the warp. BATCH rows' residuals are in flight at a time
+// (4608 x 9218 x 16 in batches of 8 and of 32: 89 and 43 us, with a residual 277 and 187).
+template <bool OUT32, bool FULL, int BATCH>
 __device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t* box, int lane, int row0, int col) {
   const int rows = e.m - row0 < 32 ? e.m - row0 : 32;
   if (col >= e.n) return;
@@ -287,46 +288,46 @@ __device__ __forceinline__ void lin_finish_column(const LinEpi& e, const uint8_t
   const int act = FULL ? e.act : kActNone;
   const uint8_t* src = box + (lane & 3) * 4;
 #pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    float z[8], res[8];
+  for (int r0 = 0; r0 < rows; r0 += BATCH) {
+    float z[BATCH], res[BATCH];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      z[i] = *reinterpret_cast<const float*>(src + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4)) + bias;
+    for (int i = 0; i < BATCH; ++i) {
+      z[i] = *reinterpret_cast<const float*>(src + (r0 + i) * 128 + (((lane >> 2) ^ (i & 7)) << 4)) + bias;
       res[i] = 0.f;
     }
     if (has_res) {
       if (res_f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < BATCH; ++i)
           if (r0 + i < rows) res[i] = r32[i * res_ld];
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < BATCH; ++i)
           if (r0 + i < rows) res[i] = __bfloat162float(r16[i * res_ld]);
       }
-      r32 += 8 * res_ld;
-      r16 += 8 * res_ld;
+      r32 += BATCH * res_ld;
+      r16 += BATCH * res_ld;
     }
     if (has_z) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < BATCH; ++i)
         if (r0 + i < rows) z16[i * z_ld] = __float2bfloat16_rn(z[i]);
-      z16 += 8 * z_ld;
+      z16 += BATCH * z_ld;
     }
     if (act != kActNone) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = lin_act(z[i], act);
+      for (int i = 0; i < BATCH; ++i) z[i] = lin_act(z[i], act);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < BATCH; ++i) {
       const float y = fmaf(alpha, z[i], res[i]);
       if (r0 + i < rows) {
         if (OUT32) o32[i * out_ld] = y;
         else o16[i * out_ld] = __float2bfloat16_rn(y);
       }
     }
-    o32 += 8 * out_ld;
-    o16 += 8 * out_ld;
+    o32 += BATCH * out_ld;
+    o16 += BATCH * out_ld;
   }
 }
 
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         boxes_free();
         lin_box_write(boxes, lane, v, true, 0);
         __syncwarp();
-        lin_finish_column<FINE, FULL>(e, boxes, lane, row0, col + lane);
+        lin_finish_column<FINE, FULL, FINE ? 8 : 32>(e, boxes, lane, row0, col + lane);
         return;
       }
       if (has_bias) {
