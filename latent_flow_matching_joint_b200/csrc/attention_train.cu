@@ -41,12 +41,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kFwdBar = 6 * kAtTile;     // 2 query tiles, 2 stages of K, 2 of V
 constexpr int kFwdSmem = kFwdBar + 256 + 1024;
 
-#ifndef KLEIN_BWD_WARPS
-#define KLEIN_BWD_WARPS 16
-#endif
-constexpr int kBwdWarps = KLEIN_BWD_WARPS;         // elementwise warps of the backward kernel
+constexpr int kBwdWarps = 16;                      // elementwise warps of the backward kernel (8: 2 % slower)
 constexpr int kBwdThreads = 64 + 32 * kBwdWarps;
 constexpr int kBwdCols = 128 / (kBwdWarps / 4);    // columns of a tile per warp
+static_assert(kBwdCols == 32, "a warp's columns are one tensor-memory load");
 // Shared memory: 2 resident tiles, a ring of 3 of the first streamed tile (it
 // is needed from the scores to the end of its step, and the next step's scores
 // are made half a step ahead), a ring of 2 of the second, with the statistics.
@@ -58,13 +56,8 @@ constexpr int kBwdBar = kBwdStat + 2 * kStatBytes;
 constexpr int kBwdSmem = kBwdBar + 256;
 static_assert(kBwdSmem <= 227 * 1024, "shared memory of one CTA");
 
-// Descriptor of 16 rows of a tile as the contraction (the operand's own index,
-// d, is the contiguous one): next 64 d one box later, next 8 rows 1 KB later.
-__device__ __forceinline__ uint64_t across_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kAtBox >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
-}
+// 16 rows of a tile as the contraction (d, the contiguous index, is the operand's own).
+__device__ __forceinline__ uint64_t across_desc(uint32_t saddr) { return sw128_desc_mn(saddr, kAtBox); }
 
 constexpr uint32_t kIdescAlong = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescAcross = kIdescAlong | (1u << 16);  // B is contiguous along its own index
@@ -170,18 +163,6 @@ __device__ __forceinline__ void mma_across_bwd(uint32_t d_tmem, uint32_t a_tmem,
                           kIdescAcross, accumulate || kk != 0);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float* v) {
-  if (N == 64) tmem_ld64(taddr, v);
-  else tmem_ld32(taddr, v);
-}
-
-template <int N>  // N packed columns
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* v) {
-  if (N == 32) tmem_st32(taddr, reinterpret_cast<const float*>(v));
-  else tmem_st16(taddr, v);
-}
-
 __device__ __forceinline__ __nv_bfloat16* head_row(const HeadsView& v, int b, int head, int row) {
   return static_cast<__nv_bfloat16*>(v.data) + b * v.batch_stride + head * v.head_stride + row * v.row_stride;
 }
@@ -189,9 +170,12 @@ __device__ __forceinline__ __nv_bfloat16* head_row(const HeadsView& v, int b, in
 }  // namespace
 
 // Forward. One CTA = two query slots (a, b) of one head, sharing every K/V
-// tile; roles and pipeline as in the denoiser's attention kernel (warp 0 TMA,
-// warp 1 MMA, warps 2..5 and 6..9 the softmax of slot a and b, one query row
-// per thread; P written over S in tensor memory and fed from there).
+// tile; roles and pipeline as in the denoiser's attention kernel (320 threads:
+// warp 0 TMA, warp 1 MMA, warps 2..5 and 6..9 the softmax of slot a and b, one
+// query row per thread; P written over S in tensor memory and fed from there).
+// Bound by each row's chain of scores, maximum, exponentials and P: the tensor
+// pipe and the MUFU are both 61 % busy. 24 heads, 4608 rows: 210 us in short
+// bursts (1240 TFLOP/s).
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_train_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const AttnTrainArgs a) {
@@ -493,8 +477,8 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
 // same bits every run. Both kinds are one grid, so that the second fills the
 // SMs that the first leaves at its end.
 //
-// Roles (320 threads): warp 0 TMA, warp 1 MMA issue, warps 2..9 elementwise,
-// two per TMEM lane quarter, each with half of the tile's columns. P and dS are
+// Roles (576 threads): warp 0 TMA, warp 1 MMA issue, warps 2..17 elementwise,
+// four per TMEM lane quarter, each with 32 of the tile's columns. P and dS are
 // packed to bf16 over the scores they came from (each warp over its own
 // columns) and fed to the next product from tensor memory.
 //
@@ -504,6 +488,11 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
 // while they make dS_j it runs dV_j and S_{j+1}.
 // dQ block: lanes are queries, columns keys. S = Q K^T (two buffers), dP = dO V^T,
 // dQ += dS K.
+//
+// Measured (24 heads, 4608 rows): 700 us in short bursts, 930 TFLOP/s counted as 5 products; 840 in a long loop, at
+// the power cap. A dK/dV step takes 3050 clocks for 2048 of tensor work: it waits about 700 for P, whose 16384
+// exponentials alone take 1024 (half of them as polynomials on the FMA pipe: 1.5 % faster in all, not kept). A dQ step
+// takes 2230 for 1536. CTA pairs, each CTA with half of every streamed operand, were no faster (785 against 764 then).
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_train_bwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
@@ -742,7 +731,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float p[kC], d[kC];
     uint32_t pk[kC / 2];
     auto hand_over = [&](uint32_t col, uint64_t* bar) {  // the packed values, to the MMA warp
-      tmem_st_cols<kC / 2>(col, pk);
+      tmem_st16(col, pk);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
@@ -754,7 +743,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float4* dd = lse + 32;
         if (!mbar_wait_warp(&t_in[j & 1], (j >> 1) & 1, 0x417) || !mbar_wait_warp(&s_full[0], j & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld_cols<kC>(lane_base, p);
+        tmem_ld32(lane_base, p);
 #pragma unroll
         for (int i = 0; i < kC; i += 4) {
           const float4 m = lse[i >> 2];
@@ -768,7 +757,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         hand_over(lane_base, p_ready);
         if (!mbar_wait_warp(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld_cols<kC>(lane_base + 128, d);
+        tmem_ld32(lane_base + 128, d);
 #pragma unroll
         for (int i = 0; i < kC; i += 4) {
           const float4 m = dd[i >> 2];
@@ -784,7 +773,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int j = 0; j < n; ++j) {
         if (!mbar_wait_warp(&s_full[j & 1], (j >> 1) & 1, 0x417)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld_cols<kC>(lane_base + (j & 1) * 128, p);
+        tmem_ld32(lane_base + (j & 1) * 128, p);
 #pragma unroll
         for (int i = 0; i < kC; i += 2) {
           ffma2(p[i], p[i + 1], p[i], p[i + 1], sl2, sl2, -lse, -lse);
@@ -798,7 +787,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!mbar_wait_warp(dp_full, j & 1, 0x418)) { ok = false; break; }
         tc_fence_after();
-        tmem_ld_cols<kC>(lane_base + 256, d);
+        tmem_ld32(lane_base + 256, d);
 #pragma unroll
         for (int i = 0; i < kC; i += 2) pk[i >> 1] = pack_bf16(p[i] * (d[i] - dd), p[i + 1] * (d[i + 1] - dd));
         hand_over(lane_base + 256, ds_ready);
@@ -812,7 +801,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (finished && n > 0) {
       tc_fence_after();
       auto stage = [&](int at, uint32_t col, float f) {
-        tmem_ld_cols<kC>(lane_base + col, d);
+        tmem_ld32(lane_base + col, d);
         uint8_t* row = sm_s + at * kAtTile + rloc * 256;
 #pragma unroll
         for (int i = 0; i < kC; i += 8)

@@ -210,7 +210,7 @@ struct LinDzArgs {
   int n, slab;          // slab: rows per block (lin_dz_slab)
   const void* dout;
   long long dout_ld;
-  int dout_f32, dout_vec;
+  int dout_f32, dout_vec;  // dout_vec, z_vec: bf16, eight columns may be loaded at once
   const __nv_bfloat16* z;
   long long z_ld;
   int z_vec, act;

@@ -1426,7 +1426,7 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
     d.dout = a->dout;
     d.dout_ld = a->dout_ld;
     d.dout_f32 = a->dout_f32 != 0;
-    d.dout_vec = aligned16(a->dout) && (a->dout_ld % (d.dout_f32 ? 4 : 8)) == 0;
+    d.dout_vec = !d.dout_f32 && aligned16(a->dout) && (a->dout_ld % 8) == 0;
     d.z = static_cast<const __nv_bfloat16*>(a->preact);
     d.z_ld = a->preact_ld;
     d.z_vec = aligned16(a->preact) && (a->preact_ld % 8) == 0;

@@ -53,17 +53,6 @@ constexpr int kLinChunk = 8;                   // FINE: k blocks (of 64) per TME
 constexpr int kLinSms = 148;                   // the B200's SM count: plans and workspace sizes do not depend on the device
 constexpr int kLinPairs = kLinSms / 2;
 
-// Shared-memory descriptor of an operand tile that is contiguous along its
-// row index (MN-major), written by TMA in boxes of 64 rows x 64 k with
-// 128-byte swizzling: lines of 64 row indices (128 B), 8 k per 1 KB atom
-// (stride byte offset), the next 64 row indices one box later (leading byte
-// offset).
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t box_bytes) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(box_bytes >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
-}
-
 __device__ __forceinline__ float lin_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -862,7 +851,7 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(const LinDzArgs a) {
       }
     }
   };
-  if (count == 8 && a.dout_vec && !a.dout_f32 && (ACT == kActNone || a.z_vec)) {
+  if (count == 8 && a.dout_vec && (ACT == kActNone || a.z_vec)) {
     // Four rows' loads in flight per warp and the registers that takes (two blocks per SM): 4608 x 9216 with GELU in
     // about 57 us (255 MB, floor 39). Three blocks per SM spill: 94; two rows and four blocks 60; one row and six 84.
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(a.dout) + col;
