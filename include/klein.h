@@ -418,7 +418,9 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
  * attention with its row statistics, a linear layer with its epilogue, and
  * the gradients of both. Same conventions as
  * above. Results do not depend on the order in which the GPU runs things: the
- * same call gives the same bits. */
+ * same call gives the same bits. Outputs must not overlap inputs or one another
+ * except where a call says so; one at an input's address is refused
+ * (KLEIN_ERR_INVALID_ARG). */
 
 /* A bf16 tensor [batch][heads][rows][128] in any layout with contiguous heads'
  * vectors: the distance between neighbours along each axis, in elements.

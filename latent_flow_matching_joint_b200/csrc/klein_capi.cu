@@ -1170,6 +1170,19 @@ int klein_op_attention(const void* q, const void* k, const void* vt, int batch, 
 
 static bool element_aligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) == 0; }
 
+// Whether one of `outputs` starts where an input or another output does (the
+// one overlap that is certainly a mistake; others are the caller's to avoid).
+static bool same_address(const void* const* outputs, int n_out, const void* const* inputs, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!outputs[i]) continue;
+    for (int j = 0; j < n_in; ++j)
+      if (outputs[i] == inputs[j]) return true;
+    for (int j = 0; j < i; ++j)
+      if (outputs[i] == outputs[j]) return true;
+  }
+  return false;
+}
+
 // Checks a [batch][heads][rows][128] view and returns it with usable strides
 // for axes of length one (they are never stepped along, but the tensor map
 // wants a multiple of 16 bytes). `written`: no element may have two indices.
@@ -1238,6 +1251,9 @@ int klein_op_attention_forward(const klein_attention_shape* shape, const klein_h
     return rc;
   if (!lse) return fail(KLEIN_ERR_INVALID_ARG, "lse is NULL");
   if (!element_aligned(lse, 1)) return fail(KLEIN_ERR_ALIGN, "lse is not aligned to its element");
+  const void* outs[] = {a.out.data, lse};
+  const void* ins[] = {a.q.data, a.k.data, a.v.data};
+  if (same_address(outs, 2, ins, 3)) return fail(KLEIN_ERR_INVALID_ARG, "an output is one of the inputs");
   a.lse = lse;
   rc = launch_attention_train(a, static_cast<cudaStream_t>(stream));
   if (rc == -2) return fail(KLEIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -1270,6 +1286,9 @@ int klein_op_attention_backward(const klein_attention_shape* shape, const klein_
   const size_t need = klein_attention_backward_workspace_size(a.batch, a.heads, a.rows, a.n_txt);
   if (!ws || ws_bytes < need) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", need);
   if (!aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  const void* outs[] = {a.dq.data, a.dk.data, a.dv.data, ws};
+  const void* ins[] = {a.q.data, a.k.data, a.v.data, a.out.data, a.dout.data, lse};
+  if (same_address(outs, 4, ins, 6)) return fail(KLEIN_ERR_INVALID_ARG, "an output is one of the inputs or outputs");
   a.lse = const_cast<float*>(lse);  // only read by the backward kernels
   a.stats = static_cast<float*>(ws);
   rc = launch_attention_backward(a, static_cast<cudaStream_t>(stream));
@@ -1329,6 +1348,10 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
   const size_t need = klein_linear_workspace_size(a->m, a->n, a->k);
   if (ws_bytes < need || (need && !ws)) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", need);
   if (need && !aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  const void* outs[] = {a->out, a->preact, need ? ws : nullptr};
+  const void* ins[] = {a->x, a->w, a->bias};
+  if (same_address(outs, 3, ins, 3) || (a->preact && a->preact == a->residual))
+    return fail(KLEIN_ERR_INVALID_ARG, "an output is one of the inputs or outputs");
   LinEpi e{};
   e.m = a->m;
   e.n = a->n;
@@ -1408,6 +1431,9 @@ int klein_op_linear_backward(const klein_linear_grad_args* a, void* ws, size_t w
   const LinearGradWs w = carve_linear_grad(a->m, a->n, a->k);
   if (!ws || ws_bytes < w.bytes) return fail(KLEIN_ERR_WORKSPACE, "workspace too small: need %zu bytes", w.bytes);
   if (!aligned16(ws)) return fail(KLEIN_ERR_ALIGN, "unaligned workspace");
+  const void* outs[] = {a->dx, a->dw, a->dbias, ws};
+  const void* ins[] = {a->dout, a->x, a->w, a->preact};
+  if (same_address(outs, 4, ins, 4)) return fail(KLEIN_ERR_INVALID_ARG, "an output is one of the inputs or outputs");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
   // dout itself is the products' operand when nothing but alpha separates it

@@ -135,6 +135,49 @@ def test_adapter_step_captured(kb):
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+FIRST_CALL = """
+import torch
+import latent_flow_matching_joint_b200 as kb
+def bf(*shape): return torch.randn(*shape, device="cuda").bfloat16()
+q, do, x, w = bf(1, 2, 200, 128), bf(1, 2, 200, 128), bf(1200, 1024), bf(1024, 1024)
+outs = [torch.zeros(1, 2, 200, 128, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+lse, y = torch.zeros(1, 2, 200, device="cuda"), torch.zeros(1200, 1024, device="cuda")
+dx, dw = torch.zeros(1200, 1024, device="cuda"), torch.zeros(1024, 1024, device="cuda")
+wa = torch.empty(kb.klein_attention_backward_workspace_size(1, 2, 200), dtype=torch.uint8, device="cuda")
+wl = torch.empty(max(kb.klein_linear_workspace_size(1200, 1024, 1024),
+                     kb.klein_linear_backward_workspace_size(1200, 1024, 1024)), dtype=torch.uint8, device="cuda")
+def step():
+    kb.klein_op_attention_forward(q, k, v, outs[0], lse)
+    kb.klein_op_attention_backward(q, k, v, outs[0], lse, do, *outs[1:], wa)
+    kb.klein_op_linear(x, w, y, wl)
+    kb.klein_op_linear_backward(y, x, w, wl, dx=dx, dw=dw)
+k, v = q.clone(), do.clone()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (*outs, lse, y, dx, dw)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) and a.abs().sum() > 0 for a, b in zip(got, (*outs, lse, y, dx, dw)))
+print("first call captured")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_captured(kb):
+    """Nothing that a call sets up at its first use stands in the way of a stream capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, env={**os.environ, "PYTHONPATH": root},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first call captured" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.mark.gpu
 def test_two_steps_at_once(kb):
     """Two steps on two streams, each with its own workspace."""

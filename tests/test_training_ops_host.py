@@ -143,6 +143,32 @@ def test_attention_other_refusals(kb):
     assert attention(kb, dict(n_txt=30, txt_len=A), "backward", ws_bytes=need - 1) == "KLEIN_ERR_WORKSPACE"
 
 
+def test_outputs_at_an_inputs_address_are_refused(kb):
+    """Every address apart from the pair in question."""
+    def apart(names, same):
+        at = {name: A * (i + 2) for i, name in enumerate(names)}
+        at[same[0]] = at[same[1]]
+        return at
+
+    for same in (("out", "x"), ("out", "w"), ("out", "bias"), ("preact", "out"), ("preact", "residual"), ("preact", "x")):
+        at = apart(("x", "w", "out", "bias", "preact", "residual"), same)
+        assert linear(kb, residual_ld=16, preact_ld=16, **at) == "KLEIN_ERR_INVALID_ARG", same
+    for same in (("dx", "x"), ("dx", "dout"), ("dw", "w"), ("dw", "dx"), ("dbias", "dw"), ("ws", "dout"), ("dx", "preact"),
+                 ("dbias", "ws")):
+        at = apart(("dout", "x", "w", "preact", "dx", "dw", "dbias", "ws"), same)
+        assert backward(kb, preact_ld=16, act=1, **at) == "KLEIN_ERR_INVALID_ARG", same
+
+    def views(names, same):
+        return {name: dict(data=at) for name, at in apart(names, same).items()}
+
+    for same in (("out", "q"), ("out", "k"), ("out", "v")):
+        assert attention(kb, None, "forward", lse=A * 50, **views(("q", "k", "v", "out"), same)) == "KLEIN_ERR_INVALID_ARG"
+    names = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
+    for same in (("dq", "q"), ("dq", "dout"), ("dk", "k"), ("dv", "v"), ("dv", "dk"), ("dk", "dq"), ("dq", "out")):
+        assert attention(kb, None, "backward", lse=A * 50, ws=A * 60, **views(names, same)) == "KLEIN_ERR_INVALID_ARG", same
+    assert attention(kb, None, "backward", lse=A * 50, ws=A * 50, **views(names, ("q", "k"))) == "KLEIN_ERR_INVALID_ARG"
+
+
 def test_workspace_sizes(kb):
     size = kb.klein_attention_backward_workspace_size
     # two floats per row of every slot of 128 rows; the text and the rows after it have their own slots
