@@ -303,3 +303,35 @@ def test_stream_and_graph(kb):
         torch.cuda.synchronize()
         want = run(kb, q, k, v, dout, n_txt, new)
         assert all(torch.equal(x, y) for x, y in zip((out, lse, dq, dk, dv), want))
+
+
+@pytest.mark.gpu
+def test_offsets_that_pass_32_bits(kb):
+    """The second batch row stands 2^31 elements and more behind the first, in each tensor in turn."""
+    b, heads, kv_heads, n, n_txt, lens, scale = 2, 2, 1, 200, 130, [5, 130], D ** -0.5
+    gap = (1 << 31) + 4096
+
+    def far(t):
+        size = t[0].numel()
+        flat = torch.empty(gap + size, dtype=t.dtype, device="cuda")
+        view = flat.as_strided(t.shape, (gap,) + t[0].contiguous().stride())
+        view.copy_(t)
+        return view
+
+    q, dout = (randn(s, b, heads, n, D).bfloat16() for s in (1, 2))
+    k, v = (randn(s, b, kv_heads, n, D).bfloat16() for s in (3, 4))
+    ref = Reference(q, k, v, dout, mask(b, n, n_txt, lens), scale)
+    txt_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kb.klein_attention_backward_workspace_size(b, heads, n, n_txt), dtype=torch.uint8, device="cuda")
+    for which in ("q", "k", "v", "out", "dout", "dq", "dk", "dv"):
+        t = {"q": q, "k": k, "v": v, "dout": dout, "out": torch.zeros_like(q), "dq": torch.zeros_like(q),
+             "dk": torch.zeros_like(k), "dv": torch.zeros_like(k)}
+        t[which] = far(t[which])
+        lse = torch.zeros(b, heads, n, device="cuda")
+        kb.klein_op_attention_forward(t["q"], t["k"], t["v"], t["out"], lse, n_txt=n_txt, txt_len=txt_len)
+        kb.klein_op_attention_backward(t["q"], t["k"], t["v"], t["out"], lse, t["dout"], t["dq"], t["dk"], t["dv"], ws,
+                                       n_txt=n_txt, txt_len=txt_len)
+        assert kb.klein_sync()[0] == 0
+        for name in ("out", "dq", "dk", "dv"):
+            within(f"{name}, {which} far", t[name], getattr(ref, name), getattr(ref, name + "_tol"))
+        del t

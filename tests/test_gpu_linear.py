@@ -296,3 +296,45 @@ def test_linear_on_a_stream_and_in_a_graph(kb):
     kb.klein_op_linear(x, w, want, ws, residual=r)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_offsets_that_pass_32_bits(kb):
+    """Rows of a pitch of 2^23 elements: the last ones stand 2^31 elements and more behind the first."""
+    m, n, k, pitch = 300, 264, 200, 1 << 23
+
+    def far(t):
+        flat = torch.empty((m - 1) * pitch + t.shape[1], dtype=t.dtype, device="cuda")
+        view = flat.as_strided(t.shape, (pitch, 1))
+        view.copy_(t)
+        return view
+
+    w = (randn(1, n, k) / math.sqrt(k)).bfloat16()
+    ws = torch.empty(kb.klein_linear_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+    wsb = torch.empty(kb.klein_linear_backward_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+    # One far tensor at a time: x, the residual and output in place, the saved sums, then dout and dx.
+    x, r = randn(0, m, k).bfloat16(), randn(2, m, n).bfloat16()
+    for which in ("x", "out", "z"):
+        y = far(r) if which == "out" else r.clone()
+        z = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+        z = far(z) if which == "z" else z
+        kb.klein_op_linear(far(x) if which == "x" else x, w, y, ws, residual=y, act="silu", preact=z)
+        assert kb.klein_sync()[0] == 0
+        zr = x.double() @ w.double().T
+        ref = act64(zr, "silu") + r.double()
+        tol = 1.13 * SUM + 1e-5 * zr.abs() + HALF[torch.bfloat16] * ref.abs() + 1e-7
+        assert ((y.double() - ref).abs() <= tol).all(), which
+        assert ((z.double() - zr).abs() <= SUM + (1e-5 + HALF[torch.bfloat16]) * zr.abs()).all(), which
+        del y, z
+    dout = randn(3, m, n).bfloat16()
+    for which in ("dout", "dx"):
+        dx = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+        dx = far(dx) if which == "dx" else dx
+        dw = torch.zeros(n, k, dtype=torch.float32, device="cuda")
+        kb.klein_op_linear_backward(far(dout) if which == "dout" else dout, x, w, wsb, dx=dx, dw=dw)
+        assert kb.klein_sync()[0] == 0
+        dxr, dwr = dout.double() @ w.double(), dout.double().T @ x.double()
+        dxs, dws = dout.double().abs() @ w.double().abs(), dout.double().abs().T @ x.double().abs()
+        assert ((dx.double() - dxr).abs() <= HALF[torch.bfloat16] * dxr.abs() + SUM * dxs).all(), which
+        assert ((dw.double() - dwr).abs() <= HALF[torch.float32] * dwr.abs() + SUM * dws).all(), which
+        del dx
