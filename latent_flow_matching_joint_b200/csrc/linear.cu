@@ -844,10 +844,12 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(const LinDzArgs a) {
           make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
       *reinterpret_cast<uint4*>(a.dz + r * a.dz_ld + col) = hi;
       if (a.low) {  // what the rounding left, rounded in turn
-        const float2 h0 = unpack_bf16(hi.x), h1 = unpack_bf16(hi.y), h2 = unpack_bf16(hi.z), h3 = unpack_bf16(hi.w);
+        float h[8];
+        unpack8(hi, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = fabsf(h[i]) <= 3.4e38f ? d[i] - h[i] : 0.f;  // none for infinities and NaN
         *reinterpret_cast<uint4*>(a.dz + r * a.dz_ld + a.low + col) =
-            make_uint4(pack_bf16(d[0] - h0.x, d[1] - h0.y), pack_bf16(d[2] - h1.x, d[3] - h1.y),
-                       pack_bf16(d[4] - h2.x, d[5] - h2.y), pack_bf16(d[6] - h3.x, d[7] - h3.y));
+            make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
       }
     }
   };

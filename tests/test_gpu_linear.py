@@ -338,3 +338,32 @@ def test_offsets_that_pass_32_bits(kb):
         assert ((dx.double() - dxr).abs() <= HALF[torch.bfloat16] * dxr.abs() + SUM * dxs).all(), which
         assert ((dw.double() - dwr).abs() <= HALF[torch.float32] * dwr.abs() + SUM * dws).all(), which
         del dx
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(64, 128, 72), (700, 2056, 520)])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_infinite_gradients_stay_infinite(kb, m, n, k, act):
+    """One infinity in dout: fp32 gradients have it, with its sign, where the sums do, and nothing else changes."""
+    x, w = randn(0, m, k).bfloat16(), randn(1, n, k).bfloat16()
+    x[x == 0], w[w == 0] = 1, 1
+    z = randn(2, m, n).abs().bfloat16() + 1  # act' > 0
+    dout = randn(3, m, n)
+    ws = torch.empty(kb.klein_linear_backward_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+
+    def grads():
+        dx, dw, db = (torch.zeros(s, device="cuda") for s in ((m, k), (n, k), (n,)))
+        kb.klein_op_linear_backward(dout, x, w, ws, dx=dx, dw=dw, dbias=db, preact=z, act=act)
+        assert kb.klein_sync()[0] == 0
+        return dx, dw, db
+
+    before = grads()
+    i, j = m - 3, n // 2 + 1
+    dout[i, j] = -math.inf
+    dx, dw, db = grads()
+    assert torch.equal(dx[i], -math.inf * w[j].float())
+    assert torch.equal(dw[j], -math.inf * x[i].float())
+    assert db[j] == -math.inf
+    for got, old, row in ((dx, before[0], i), (dw, before[1], j), (db, before[2], j)):
+        got[row] = old[row]
+        assert torch.equal(got, old)
