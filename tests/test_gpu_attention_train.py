@@ -5,7 +5,8 @@ H = 2^-8 of it):
   out   H |out| for the output, H sum_j p_ij |v_j| for the probabilities
   lse   fp32 arithmetic: 128 products per score, the fast exponential and logarithm (1e-5 of the scores' size)
   dv    H |dv| + H sum_i p_ij |do_i|
-  dS    H |dS| for its rounding; P times the error of D = sum_d do o, whose o carries H |o|
+  dS    H |dS| for its rounding; P times the error of D = sum_d do o, whose o carries H |o| (over up to 16 keys
+        D is summed from the inputs and has only fp32's error)
   dq, dk   H of the result + scale times (error of dS) times |k| or |q|
 FP32 = 3e-5 of the products' magnitudes covers fp32 sums, the recomputed scores and exponentials.
 """
@@ -55,7 +56,7 @@ def mask(batch, n, n_txt, lens):
 class Reference:
     """The formulas in float64 with padding rows taken out, and the error bounds."""
 
-    def __init__(self, q, k, v, dout, use, scale):
+    def __init__(self, q, k, v, dout, use, scale, few_keys=False):
         group = q.shape[1] // k.shape[1]
         zero = torch.zeros((), dtype=torch.float64, device="cuda")
         row = use[:, None, :, None]
@@ -73,7 +74,9 @@ class Reference:
         dp = do @ v.transpose(2, 3)
         ds = p * (dp - delta)
         mag = p * (do.abs() @ v.abs().transpose(2, 3) + (do * self.out).abs().sum(-1, keepdim=True))
-        ds_err = H * ds.abs() + p * H * (do * self.out).abs().sum(-1, keepdim=True) + FP32 * (1 + size) * mag
+        ds_err = H * ds.abs() + FP32 * (1 + size) * mag
+        if not few_keys:
+            ds_err = ds_err + p * H * (do * self.out).abs().sum(-1, keepdim=True)
 
         def shared(t):
             return t.reshape(t.shape[0], -1, group, t.shape[2], D).sum(2)
@@ -335,3 +338,23 @@ def test_offsets_that_pass_32_bits(kb):
         for name in ("out", "dq", "dk", "dv"):
             within(f"{name}, {which} far", t[name], getattr(ref, name), getattr(ref, name + "_tol"))
         del t
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv_heads,n,n_txt,lens", [
+    (2, 2, 1, 0, None), (2, 1, 2, 0, None), (24, 24, 3, 0, None), (4, 2, 8, 0, None), (3, 1, 9, 0, None), (2, 2, 16, 0, None),
+    (2, 1, 2, 1, [0, 1]), (4, 2, 302, 300, [0, 14]), (4, 4, 200, 200, [1, 16]), (2, 2, 140, 129, [0, 5])])
+def test_few_keys(kb, heads, kv_heads, n, n_txt, lens):
+    """Over up to 16 keys the output's rounding is not in dq and dk; padding rows hold NaN."""
+    b, scale = 2, D ** -0.5
+    q, dout = (randn(s, b, heads, n, D).bfloat16() for s in (1, 2))
+    k, v = (randn(s, b, kv_heads, n, D).bfloat16() for s in (3, 4))
+    use = mask(b, n, n_txt, lens)
+    for t in (q, dout, k, v):
+        t.masked_fill_(~use[:, None, :, None], float("nan"))
+    ref = Reference(q, k, v, dout, use, scale, few_keys=True)
+    out, lse, dq, dk, dv = run(kb, q, k, v, dout, n_txt, lens)
+    rows = use[:, None, :, None]
+    for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+        within(name, got, getattr(ref, name), torch.nan_to_num(getattr(ref, name + "_tol"), nan=0.0))
+        assert (got.masked_select(~rows) == 0).all(), name
