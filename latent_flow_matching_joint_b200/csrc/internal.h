@@ -170,7 +170,7 @@ struct LinEpi {
 
 struct LinGemmArgs {
   int m_tiles, n_tiles, k_blocks;
-  int k_wrap, a_low;   // from step k_wrap on, A's columns a_low further on against B's from the start
+  int a_low;           // > 0 (fp32 output only): every piece's k a second time, with A's columns a_low further on
   int waves, whole;    // the first `whole` tiles are dealt out whole, in `waves` rounds
   int pairs;           // CTA pairs that the work is dealt out to
   int cut, parts;      // the last `cut` tiles are cut along k into `parts` equal parts each

@@ -32,6 +32,12 @@
 // the epilogue warps' registers with rounding to nearest, while the tensor
 // core fills the other accumulator; these warps take registers over from the
 // first four (3 x 168 = 72 + 2 x 216 per thread).
+//
+// An operand in two bf16 halves (dz and its remainders, for fp32 gradients) is
+// multiplied in two passes over the same k, within every piece of work: first the
+// high halves, then the low ones in chunks of their own. What is infinite in
+// B is so in the first sum, with the right sign; the remainder's product with
+// it (0 x inf, or an infinity of either sign) is left out.
 #include "common.cuh"
 #include "internal.h"
 
@@ -390,7 +396,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
           for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
             const int row = p.mi * 256 + 128 * rank, col = p.ni * 256 + 128 * rank;
-            for (int kb = p.kb0; kb < p.kb1; ++kb) {
+            const int len = p.kb1 - p.kb0, steps = g.a_low ? 2 * len : len;
+            for (int j = 0; j < steps; ++j) {
               if (!mbar_wait(&empty[stage], phase ^ 1, 0x301)) { ok = false; break; }
               if (leader) {
                 mbar_arrive_expect_tx(&full[stage], 2 * kLinStage);
@@ -399,20 +406,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               uint8_t* sa = smem + stage * kLinStage;
               uint8_t* sb = sa + kLinTile;
               const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-              // the second pass over k reads A's low halves against the same B
-              const int kb_b = kb >= g.k_wrap ? kb - g.k_wrap : kb;
+              // the second pass over the piece's k reads A's low halves against the same B
+              const int low = j < len ? 0 : g.a_low;
+              const int k = (p.kb0 + (j < len ? j : j - len)) * 64;
               if (AMN) {
-                const int r = kb >= g.k_wrap ? row + g.a_low : row;
-                tma_load_2d_pair(sa, &map_a, bar, r, kb_b * 64);
-                tma_load_2d_pair(sa + kLinTile / 2, &map_a, bar, r + 64, kb_b * 64);
+                tma_load_2d_pair(sa, &map_a, bar, row + low, k);
+                tma_load_2d_pair(sa + kLinTile / 2, &map_a, bar, row + low + 64, k);
               } else {
-                tma_load_2d_pair(sa, &map_a, bar, kb >= g.k_wrap ? kb_b * 64 + g.a_low : kb * 64, row);
+                tma_load_2d_pair(sa, &map_a, bar, k + low, row);
               }
               if (BMN) {
-                tma_load_2d_pair(sb, &map_b, bar, col, kb_b * 64);
-                tma_load_2d_pair(sb + kLinTile / 2, &map_b, bar, col + 64, kb_b * 64);
+                tma_load_2d_pair(sb, &map_b, bar, col, k);
+                tma_load_2d_pair(sb + kLinTile / 2, &map_b, bar, col + 64, k);
               } else {
-                tma_load_2d_pair(sb, &map_b, bar, kb_b * 64, col);
+                tma_load_2d_pair(sb, &map_b, bar, k, col);
               }
               if (++stage == kLinStages) { stage = 0; phase ^= 1; }
             }
@@ -431,14 +438,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         bool ok = true;
         for (int pair = pair0; ok && pair < g.pairs; pair += pairs) {
           for (int i = 0; ok && lin_piece(g, pair, i, p); ++i) {
-            for (int kb = p.kb0; ok && kb < p.kb1; ++chunk) {
+            const int len = p.kb1 - p.kb0, steps = g.a_low ? 2 * len : len;
+            for (int j = 0; ok && j < steps; ++chunk) {
               const int acc = chunk & 1;
               if (!mbar_wait(&acc_empty[acc], ((chunk >> 1) & 1) ^ 1, 0x302)) { ok = false; break; }
               tc_fence_after();
               const uint32_t d = tmem_base + acc * 256;
-              const int first = kb;
-              const int end = FINE && kb + kLinChunk < p.kb1 ? kb + kLinChunk : p.kb1;
-              for (; kb < end; ++kb) {
+              const int first = j;
+              int end = j < len ? len : steps;  // no chunk holds steps of both passes
+              if (FINE && j + kLinChunk < end) end = j + kLinChunk;
+              for (; j < end; ++j) {
                 if (!mbar_wait(&full[stage], phase, 0x303)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t a0 = smem_u32(smem + stage * kLinStage);
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 for (int k = 0; k < 4; ++k) {
                   const uint64_t da = AMN ? sw128_desc_mn(a0 + 2048 * k, kLinTile / 2) : sw128_desc(a0 + 32 * k);
                   const uint64_t db = BMN ? sw128_desc_mn(b0 + 2048 * k, kLinTile / 2) : sw128_desc(b0 + 32 * k);
-                  umma_bf16_pair(d, da, db, idesc, kb != first || k != 0);
+                  umma_bf16_pair(d, da, db, idesc, j != first || k != 0);
                 }
                 umma_commit_pair(&empty[stage], 0x3);
                 if (++stage == kLinStages) { stage = 0; phase ^= 1; }
@@ -593,7 +602,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (pieces > 4) pieces = 4;
         if (load_res && p.slot < 0 && lane == 0 && pieces > 0) fetch_res(row0, col0);  // under the main loop
         if (FINE) {
-          const int chunks = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
+          const int high = (p.kb1 - p.kb0 + kLinChunk - 1) / kLinChunk;
+          const int chunks = g.a_low ? 2 * high : high;
           float acc[128];
           for (int c = 0; c < chunks; ++c, ++chunk) {
             const int buf = chunk & 1;
@@ -608,8 +618,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               } else {
                 float v[32];
                 tmem_ld32(taddr + 32 * j, v);
+                if (FULL || c < high) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) acc[32 * j + q] += v[q];
+                  for (int q = 0; q < 32; ++q) acc[32 * j + q] += v[q];
+                } else {  // the low halves: nothing to a sum that B has made infinite or NaN
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) acc[32 * j + q] += fabsf(acc[32 * j + q]) < INFINITY ? v[q] : 0.f;
+                }
               }
             }
             release(buf);
@@ -915,8 +930,8 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float* part, in
 
 // ------------------------------------------------------------------ host
 
-// How one product's tiles are dealt out, from its sizes alone (k already
-// counted twice where A has low halves). Costs in clocks at 1.9 GHz: a 64-deep
+// How one product's tiles are dealt out, from its sizes alone (k_blocks
+// counts k twice where A has low halves). Costs in clocks at 1.9 GHz: a 64-deep
 // step of a 256 x 256 tile takes about 750 with all pairs at work, a part
 // 1500 more for filling and emptying its pipeline, the second launch 5000, and
 // the parts' sums go to L2 and back at about 4000 bytes per clock.
@@ -1008,8 +1023,7 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
   LinGemmArgs g{};
   g.m_tiles = plan.m_tiles;
   g.n_tiles = plan.n_tiles;
-  g.k_blocks = kb * passes;
-  g.k_wrap = kb;
+  g.k_blocks = kb;
   g.a_low = a.low;
   g.waves = plan.waves;
   g.whole = plan.whole;
@@ -1031,6 +1045,7 @@ int launch_linear_gemm(const LinOperand& a, const LinOperand& b, int k, const Li
     return -2;
   int rc;
   const bool fine = epi.out_f32, full = epi.bias || epi.z || epi.act != kActNone;
+  if (a.low && (!fine || full)) return -2;  // low halves are summed in registers, without an epilogue
   if (a.mn_major) {
     if (full) return -2;
     rc = fine ? launch_lin_one<true, true, true, false>(ma, mb, mo, mr, g, s)

@@ -1,0 +1,68 @@
+"""GPU tests of klein_op_linear_backward where its fp32 gradients carry remainders: values that are not finite, and the
+activations' derivatives in their tails."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_linear import kb, pitched, randn  # noqa: E402,F401
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(64, 128, 72), (700, 2056, 520), (2100, 2312, 2056), (5000, 264, 136), (80, 5000, 100)])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_infinite_operands_stay_infinite(kb, m, n, k, act):
+    """One infinity in w, then in x: fp32 gradients are infinite where their sums are, of the sign of dz, and have their
+    old bits elsewhere (with an fp32 dout they are sums of two products, one of dz in bf16 and one of what that left).
+    Two infinities against the same sign of dz are one, against both signs a NaN."""
+    x, w = pitched(randn(0, m, k).bfloat16()), pitched(randn(1, n, k).bfloat16())
+    z = randn(2, m, n).abs().bfloat16() + 1  # act' > 0
+    dout = randn(3, m, n)
+    dout[dout == 0] = 1
+    dout[:, 3] = dout[:, 3].bfloat16().float()  # some remainders are 0 with act none
+    dout[5] = dout[5].bfloat16().float()
+    ws = torch.empty(kb.klein_linear_backward_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+
+    def grads():
+        dx, dw = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+        kb.klein_op_linear_backward(dout, x, w, ws, dx=dx, dw=dw, preact=z, act=act)
+        assert kb.klein_sync()[0] == 0
+        return dx, dw
+
+    dx0, dw0 = grads()
+    assert torch.isfinite(dx0).all() and torch.isfinite(dw0).all()
+    for rows in ((3,), (n - 1,), (3, n // 2)):  # w's rows; n - 1 lies in the last part of a cut contraction
+        kept = w[list(rows), 7].clone()
+        w[list(rows), 7] = math.inf
+        dx, dw = grads()
+        want = dx0.clone()
+        want[:, 7] = sum(dout[:, j] * math.inf for j in rows)
+        assert torch.equal(dx.nan_to_num(1e38), want.nan_to_num(1e38)) and torch.equal(dx.isnan(), want.isnan()), rows
+        assert torch.equal(dw, dw0)
+        w[list(rows), 7] = kept
+    for rows in ((5,), (m - 1,), (5, m // 2)):
+        kept = x[list(rows), 9].clone()
+        x[list(rows), 9] = -math.inf
+        dx, dw = grads()
+        want = dw0.clone()
+        want[:, 9] = sum(dout[i] * -math.inf for i in rows)
+        assert torch.equal(dw.nan_to_num(1e38), want.nan_to_num(1e38)) and torch.equal(dw.isnan(), want.isnan()), rows
+        assert torch.equal(dx, dx0)
+        x[list(rows), 9] = kept
+
+
+@pytest.mark.gpu
+def test_nan_operands_stay_nan(kb):
+    m, n, k = 700, 2056, 520
+    x, w, dout = randn(0, m, k).bfloat16(), randn(1, n, k).bfloat16(), randn(3, m, n)
+    w[n - 2, 4] = math.nan
+    x[m - 2, 6] = math.nan
+    ws = torch.empty(kb.klein_linear_backward_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+    dx, dw = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    kb.klein_op_linear_backward(dout, x, w, ws, dx=dx, dw=dw)
+    assert kb.klein_sync()[0] == 0
+    for got, col in ((dx, 4), (dw, 6)):
+        assert torch.isnan(got[:, col]).all()
+        got[:, col] = 0
+        assert torch.isfinite(got).all()
