@@ -72,12 +72,14 @@ __device__ __forceinline__ float lin_act(float z, int act) {
 }
 
 // act'(z). silu' = s + z s (1 - s); gelu' = s + z s (1 - s) d(2u)/dz with s = sigmoid(2u).
-// Past |z| = 40 both are 0 or 1 to the last bit while z or z^3 may overflow:
-// they are taken at 40 there (a NaN stays).
+// s and s - s^2 keep their relative precision down to an exponent of -87, where
+// e^87 is the last denominator below 2^126 (s is 0 past it). At |z| = 100 both
+// derivatives are 0 or 1, and z is taken there from then on: further out z^3 or
+// an infinite z would meet that 0 (a NaN stays).
 template <int ACT>
 __device__ __forceinline__ float lin_act_grad(float z) {
   if (ACT == kActNone) return 1.0f;
-  z = fabsf(z) > 40.0f ? copysignf(40.0f, z) : z;
+  z = fabsf(z) > 100.0f ? copysignf(100.0f, z) : z;
   const float z2 = z * z;
   const float s = lin_sigmoid(ACT == kActSilu ? z : kGelu2C * z * fmaf(kGeluA, z2, 1.0f));
   const float t = z * (s - s * s);

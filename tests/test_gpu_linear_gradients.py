@@ -66,3 +66,48 @@ def test_nan_operands_stay_nan(kb):
         assert torch.isnan(got[:, col]).all()
         got[:, col] = 0
         assert torch.isfinite(got).all()
+
+
+def derivative(z, act):
+    """(act'(z), the size of the terms it is the sum of, the exponent's argument) in float64."""
+    if act == "silu":
+        u, du = z, torch.ones_like(z)
+    else:
+        c = 2 * math.sqrt(2 / math.pi)
+        u, du = c * (z + 0.044715 * z ** 3), c * (1 + 3 * 0.044715 * z ** 2)
+    s, t = torch.sigmoid(u), z * du * torch.sigmoid(u) * torch.sigmoid(-u)
+    return s + t, s.abs() + t.abs(), u.abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_derivative_tails(kb, act):
+    """act' to a relative error, as long as fp32 holds it: dz = dbias of a single row with dout = 1. The exponential's
+    argument carries eight roundings of 2^-24 of its size (z^3 and its constants; the product with log2 e), each of which
+    moves the exponential by that much relative, and sixteen more of the result cover the division and the sums."""
+    end = 87.0 if act == "silu" else 9.9  # e^-87 is above fp32's least normal number
+    z = torch.cat([torch.linspace(-end, end, 4000, device="cuda"),
+                   torch.tensor([0.0, -40.0, -40.5, -60.0, 39.0, 41.0, 60.0], device="cuda").clamp(-end, end)]).bfloat16()
+    big = torch.tensor([120.0, 300.0, 1e15, 3e38, math.inf], device="cuda").bfloat16()
+    z = torch.cat([z, big, -big, torch.tensor([math.nan], device="cuda").bfloat16()])
+    n = z.numel()
+    x, w = torch.ones(1, 8, device="cuda", dtype=torch.bfloat16), torch.ones(n, 8, device="cuda", dtype=torch.bfloat16)
+    ws = torch.empty(kb.klein_linear_backward_workspace_size(1, n, 8), dtype=torch.uint8, device="cuda")
+    for dtype in (torch.bfloat16, torch.float32):
+        dout, db = torch.ones(1, n, device="cuda", dtype=dtype), torch.empty(n, device="cuda")
+        kb.klein_op_linear_backward(dout, x, w, ws, dbias=db, preact=z[None], act=act)
+        assert kb.klein_sync()[0] == 0
+        inside = n - 11
+        ref, size, arg = derivative(z[:inside].double(), act)
+        tol = 2.0 ** -24 * (8 * arg + 16) * size
+        err = (db[:inside].double() - ref).abs()
+        assert (err <= tol).all(), (z[:inside][err > tol][:5], db[:inside][err > tol][:5])
+        assert (db[inside:inside + 5] == 1).all()
+        assert (db[inside + 5:inside + 10] == 0).all()
+        assert torch.isnan(db[-1])
+        # an infinite dout keeps the derivative's sign where that is not 0
+        dout.fill_(math.inf)
+        kb.klein_op_linear_backward(dout, x, w, ws, dbias=db, preact=z[None], act=act)
+        assert kb.klein_sync()[0] == 0
+        safe = ref.abs() > 1e-3 * size
+        assert torch.equal(db[:inside][safe], (ref[safe] * math.inf).float())
