@@ -614,18 +614,20 @@ def _workspace(ws):
     return ws.data_ptr(), ws.nbytes
 
 
-def _linear_sizes(x, w, act):
+def _columns(name, t):
+    if t.dim() != 2:
+        _refuse(-2, f"{name} must be a matrix")
+    return t.shape[1]
+
+
+def _linear_sizes(m, n, k, act):
     if _torch is None:
         _load_torch()
-    if x.dim() != 2 or w.dim() != 2:
-        _refuse(-2, "x and w must be matrices")
     if act not in ACTIVATIONS:
         _refuse(-1, f"unknown activation {act!r}")
-    m, k = x.shape
-    n = w.shape[0]
     if m > INT_MAX or n > INT_MAX or k > INT_MAX:
         _refuse(-2, "matrix too large")
-    return m, n, k, ACTIVATIONS[act]
+    return ACTIVATIONS[act]
 
 
 def klein_linear_workspace_size(m: int, n: int, k: int) -> int:
@@ -638,7 +640,9 @@ def klein_op_linear(x, w, out, ws=None, bias=None, residual=None, act: str = "no
     float32 [n], residual and out bf16 or float32 [m, n] (residual may be out),
     preact bf16 [m, n] receives x w^T + bias. act: "none", "silu", "gelu" (tanh
     form). ws: klein_linear_workspace_size(m, n, k) bytes."""
-    m, n, k, act_code = _linear_sizes(x, w, act)
+    k, _ = _columns("x", x), _columns("w", w)
+    m, n = x.shape[0], w.shape[0]
+    act_code = _linear_sizes(m, n, k, act)
     bf16 = _torch.bfloat16
     dev = _device_of(x, (w, out, ws, bias, residual, preact))
     xp, x_ld, _ = _matrix("x", x, m, k, bf16)
@@ -660,14 +664,18 @@ def klein_op_linear_backward(dout, x, w, ws, dx=None, dw=None, dbias=None, preac
                              alpha: float = 1.0, stream=None):
     """Gradients of klein_op_linear: with dz = alpha * dout * act'(preact), dx = dz w,
     dw = dz^T x, dbias = dz summed over rows, each written if given. dout, dx and
-    dw bf16 or float32, dbias float32. ws: klein_linear_backward_workspace_size
-    (m, n, k) bytes."""
-    m, n, k, act_code = _linear_sizes(x, w, act)
+    dw bf16 or float32, dbias float32. x is read only for dw and w only for dx: the
+    one not needed may be None. ws: klein_linear_backward_workspace_size(m, n, k)
+    bytes (k = 1 for dbias with neither)."""
+    n = _columns("dout", dout)
+    m = dout.shape[0]
+    k = _columns("x", x) if x is not None else _columns("w", w) if w is not None else 1
+    act_code = _linear_sizes(m, n, k, act)
     bf16 = _torch.bfloat16
     dev = _device_of(dout, (x, w, ws, dx, dw, dbias, preact))
     gp, g_ld, g_f32 = _matrix("dout", dout, m, n)
-    xp, x_ld, _ = _matrix("x", x, m, k, bf16)
-    wp, w_ld, _ = _matrix("w", w, n, k, bf16)
+    xp, x_ld, _ = (None, 0, 0) if x is None else _matrix("x", x, m, k, bf16)
+    wp, w_ld, _ = (None, 0, 0) if w is None else _matrix("w", w, n, k, bf16)
     zp, z_ld, _ = (None, 0, 0) if preact is None else _matrix("preact", preact, m, n, bf16)
     dxp, dx_ld, dx_f32 = (None, 0, 0) if dx is None else _matrix("dx", dx, m, k)
     dwp, dw_ld, dw_f32 = (None, 0, 0) if dw is None else _matrix("dw", dw, n, k)

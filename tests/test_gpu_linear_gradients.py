@@ -111,3 +111,38 @@ def test_derivative_tails(kb, act):
         assert kb.klein_sync()[0] == 0
         safe = ref.abs() > 1e-3 * size
         assert torch.equal(db[:inside][safe], (ref[safe] * math.inf).float())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_operands_that_are_not_needed(kb, act):
+    """dx takes w alone, dw takes x alone, dbias neither."""
+    m, n, k = 700, 264, 520
+    x, w, dout = randn(0, m, k).bfloat16(), randn(1, n, k).bfloat16(), randn(2, m, n).bfloat16()
+    z = randn(3, m, n).bfloat16() if act != "none" else None
+    ws = torch.empty(kb.klein_linear_backward_workspace_size(m, n, k), dtype=torch.uint8, device="cuda")
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+
+    def call(xx, ww, wsp, **want):
+        kb.klein_op_linear_backward(dout, xx, ww, wsp, preact=z, act=act, **want)
+        assert kb.klein_sync()[0] == 0
+        return want
+
+    both = call(x, w, ws, dx=torch.zeros(m, k, **bf), dw=torch.zeros(n, k, **bf), dbias=torch.zeros(n, device="cuda"))
+    dx = call(None, w, ws, dx=torch.zeros(m, k, **bf))["dx"]
+    dw = call(x, None, ws, dw=torch.zeros(n, k, **bf))["dw"]
+    one = torch.empty(kb.klein_linear_backward_workspace_size(m, n, 1), dtype=torch.uint8, device="cuda")
+    db = call(None, None, one, dbias=torch.zeros(n, device="cuda"))["dbias"]
+    db2 = call(None, w, ws, dx=torch.zeros(m, k, **bf), dbias=torch.zeros(n, device="cuda"))["dbias"]
+    assert torch.equal(dx, both["dx"]) and torch.equal(dw, both["dw"])
+    assert torch.equal(db, both["dbias"]) and torch.equal(db2, both["dbias"])
+    before = kb.klein_launch_count()
+    for xx, ww, want in ((x, None, "dx"), (None, w, "dw"), (None, None, "dx"), (None, None, "dw")):
+        with pytest.raises(kb.KleinError):
+            call(xx, ww, ws, **{want: torch.zeros((m, k) if want == "dx" else (n, k), **bf)})
+    for bad in (x[:-1], x.float(), x[:, ::2], x[0], x.cpu()):  # what is given is looked at, needed or not
+        with pytest.raises(kb.KleinError):
+            call(bad, w, ws, dx=torch.zeros(m, k, **bf))
+    with pytest.raises(kb.KleinError):
+        call(x, w[:, :-8], ws, dw=torch.zeros(n, k, **bf))
+    assert kb.klein_launch_count() == before

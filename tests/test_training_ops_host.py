@@ -198,3 +198,18 @@ def test_binding_refuses_cpu_tensors(kb):
         kb.klein_op_linear(x[0], w, y)
     with pytest.raises(kb.KleinError, match="activation"):
         kb.klein_op_linear(x, w, y, act="tanh")
+
+
+def test_binding_takes_calls_without_the_operand_not_needed(kb):
+    """They come as far as the check of the device; what is given has its shape looked at."""
+    x, w, y = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(6, 8, dtype=torch.bfloat16), torch.zeros(4, 6)
+    for args, want in (((y, None, w, y), dict(dx=x)), ((y, x, None, y), dict(dw=w)), ((y, None, None, y), dict(dbias=y[0]))):
+        with pytest.raises(kb.KleinError, match="CUDA"):
+            kb.klein_op_linear_backward(*args, **want)
+    for bad in (y[0], y[None]):
+        with pytest.raises(kb.KleinError, match="matrix"):
+            kb.klein_op_linear_backward(bad, None, w, y, dx=x)
+        with pytest.raises(kb.KleinError, match="matrix"):
+            kb.klein_op_linear_backward(y, None, bad, y, dx=x)
+        with pytest.raises(kb.KleinError, match="matrix"):
+            kb.klein_op_linear(x, bad, y)
