@@ -452,10 +452,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // many keys share a row's weight |O| is well below |V| and the error goes
 // unseen; over a handful of keys it is the largest of all. Up to kStatKeys keys
 // D is therefore summed as sum_j P_j (dO V_j) from the inputs.
-// over 2, 4, 8 and 16 keys of normal inputs dQ is off by 0.24 % of its norm (the
+// Over 2, 4, 8 and 16 keys of normal inputs dQ is off by 0.24 % of its norm (the
 // roundings of dS and dQ), where O's rounding made that 0.35, 0.28, 0.27 and 0.25.
 // The whole backward pass of 4 x 24 heads takes 14.7 us with it at 8 keys and 16.9
 // at 16 (13.3 and 13.7 without; 25 at 32, where it gains nothing to speak of).
+// Those loops want 114 registers, the plain ones 30: where the rows after the text
+// are more than that many already, FEW is false and the loops are not compiled in.
+template <bool FEW>
 __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const AttnTrainArgs a) {
   const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
   float* stat = a.stats + ((static_cast<long long>(b) * a.heads + head) * a.slots + slot) * 256;
   const int keys = seq.len + a.rows - a.n_txt;
-  if (keys <= kStatKeys) {
+  if (FEW && keys <= kStatKeys) {
     const int kv_head = head / (a.heads / a.kv_heads);
     for (int i = 0; i < 8; ++i) {
       const int r = i * 16 + half;
@@ -945,7 +948,8 @@ int launch_attention_backward(const AttnTrainArgs& a, cudaStream_t s) {
   if (make_heads_map(&mq, a.q, a.rows, a.heads, a.batch) || make_heads_map(&mk, a.k, a.rows, a.kv_heads, a.batch) ||
       make_heads_map(&mv, a.v, a.rows, a.kv_heads, a.batch) || make_heads_map(&md, a.dout, a.rows, a.heads, a.batch))
     return -2;
-  cudaError_t e = launch_kernel(attn_stat_kernel, dim3(a.slots, a.heads, a.batch), dim3(256), 0, s, 1, a);
+  auto stat = a.rows - a.n_txt <= kStatKeys ? attn_stat_kernel<true> : attn_stat_kernel<false>;
+  cudaError_t e = launch_kernel(stat, dim3(a.slots, a.heads, a.batch), dim3(256), 0, s, 1, a);
   note_launch();
   if (e == cudaSuccess) {
     const int blocks = a.slots * (a.kv_heads + a.heads) * a.batch;

@@ -358,3 +358,23 @@ def test_few_keys(kb, heads, kv_heads, n, n_txt, lens):
     for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
         within(name, got, getattr(ref, name), torch.nan_to_num(getattr(ref, name + "_tol"), nan=0.0))
         assert (got.masked_select(~rows) == 0).all(), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("after", [15, 16, 17])
+def test_few_keys_border(kb, after):
+    """Items of few keys and of many in one batch, around as many rows after the text as count as few."""
+    b, heads, kv_heads, n_txt, scale = 4, 4, 2, 300, D ** -0.5
+    n, lens = n_txt + after, [0, 1, 2, 300]
+    q, dout = (randn(s, b, heads, n, D).bfloat16() for s in (1, 2))
+    k, v = (randn(s, b, kv_heads, n, D).bfloat16() for s in (3, 4))
+    use = mask(b, n, n_txt, lens)
+    for t in (q, dout, k, v):
+        t.masked_fill_(~use[:, None, :, None], float("nan"))
+    few, many = (Reference(q, k, v, dout, use, scale, few_keys=f) for f in (True, False))
+    _, _, dq, dk, dv = run(kb, q, k, v, dout, n_txt, lens)
+    for i in range(b):
+        ref = few if lens[i] + after <= 16 else many
+        for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+            within(name, got[i], getattr(ref, name)[i], torch.nan_to_num(getattr(ref, name + "_tol")[i], nan=0.0))
+            assert (got[i].masked_select(~use[i, None, :, None]) == 0).all(), name
