@@ -484,8 +484,13 @@ int klein_op_attention_backward(const klein_attention_shape* shape, const klein_
  *             x w^T + bias for klein_op_linear_backward; or NULL
  * m, n, k >= 1, any value (only x_ld and w_ld must be multiples of 8; elements
  * between k and the pitch are never used). Sums in fp32, rounded once on output.
+ * The tensor core truncates as it adds, about 1.1e-9 of a sum per element of k
+ * (1e-5 at k = 9216); for a float out its sums are taken over every 512 of k and
+ * added with rounding to nearest (under 1e-6 at any k).
  * x, w: 16-byte aligned; bias, float residual, float out: 4-byte; the others
- * 2-byte (16-byte alignment and pitches that are multiples of 4 are faster).
+ * 2-byte. Large calls are faster if out, residual and preact, those that there
+ * are, all have 16-byte aligned addresses, and pitches and n of whole 16 bytes (8
+ * bf16, 4 float).
  * ws: klein_linear_workspace_size(m, n, k) bytes, 16-byte aligned (NULL if 0);
  * one call at a time. Errors: KLEIN_ERR_INVALID_ARG, KLEIN_ERR_SHAPE,
  * KLEIN_ERR_ALIGN, KLEIN_ERR_WORKSPACE. */
@@ -513,8 +518,15 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
 
 /* Gradients of klein_op_linear from dout = dL/dout:
  *   dz = alpha * dout * act'(preact);  dx = dz w;  dw = dz^T x;  dbias = column sums of dz
- * (the residual's gradient is dout). dz is rounded to bf16, the operand type,
- * for the two products; dbias sums it unrounded.
+ * (the residual's gradient is dout). Sums as in klein_op_linear. Rounding of dz for
+ * the two products, whose operands are bf16:
+ *   - none if act is KLEIN_ACT_NONE and dout is bf16, 16-byte aligned, with a pitch
+ *     that is a multiple of 8: dout is the operand and alpha multiplies the sums;
+ *   - else, for a bf16 dx or dw, to bf16 (2^-8 of each element at most);
+ *   - else, for a float dx or dw, to two bf16 values (2^-16), which takes a
+ *     second pass over the product. Where the first pass is infinite or NaN, the
+ *     second is left out.
+ * dbias sums dz unrounded.
  *   dout    device [m][n], row pitch dout_ld >= n, float if dout_f32 else bf16
  *   x, w    as in the forward call (x is read only for dw, w only for dx; the
  *           one not needed may be NULL)
@@ -524,7 +536,9 @@ int klein_op_linear(const klein_linear_args* a, void* ws, size_t ws_bytes, void*
  *   dbias   device float [n], or NULL
  * At least one of dx, dw, dbias. Outputs must not overlap any input.
  * ws: klein_linear_backward_workspace_size(m, n, k) bytes, 16-byte aligned;
- * one call at a time. Alignment and errors as for klein_op_linear. */
+ * one call at a time. The size is enough for every act, type and choice of
+ * outputs (4 bytes per element of dz are most of it), and is asked of every call.
+ * Alignment and errors as for klein_op_linear. */
 typedef struct {
   int m, n, k;
   const void* dout;

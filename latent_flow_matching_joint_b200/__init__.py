@@ -470,6 +470,8 @@ def klein_op_time_mod(model: KleinModel, sigma: float, sigma_next: float, with_r
 # tensor before its address leaves Python: a wrong type, shape, stride or
 # device raises KleinError and nothing is enqueued. The work goes to the
 # tensors' device, on its current stream unless `stream` names another.
+# They are not autograd functions: nothing is recorded for tensors that require
+# a gradient.
 
 INT_MAX = 2 ** 31 - 1  # sizes are C ints: a larger one would arrive as another number
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}

@@ -10,7 +10,6 @@
 #include <stdint.h>
 #include <stdlib.h>
 
-#include <type_traits>
 #include <utility>
 
 namespace klein {

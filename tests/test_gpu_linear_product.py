@@ -187,3 +187,26 @@ def test_offsets_that_pass_32_bits(kb, k, cut, pitch):
         assert ((y.double() - ref).abs() <= tol).all(), which
         assert ((z.double() - zr).abs() <= SUM + (1e-5 + HALF[BF]) * zr.abs()).all(), which
         del y, z
+
+
+@pytest.mark.gpu
+def test_adapter_over_the_largest_image(kb):
+    """A rank-16 adapter over 512 text and 256 x 256 image tokens, in place on the frozen layer's output: at this
+    length its first half wants a workspace, and without one is refused."""
+    m, k, r, n = 512 + 256 * 256, 2560, 16, 640
+    x, a = randn(0, m, k).bfloat16(), (randn(1, r, k) / math.sqrt(k)).bfloat16()
+    b, y0 = (randn(2, n, r) / 4).bfloat16(), randn(3, m, n).bfloat16()
+    h, y = torch.empty(m, r, dtype=BF, device="cuda"), y0.clone()
+    sizes = [kb.klein_linear_workspace_size(m, r, k), kb.klein_linear_workspace_size(m, n, r)]
+    assert sizes[0] > 0
+    with pytest.raises(kb.KleinError, match="workspace"):
+        kb.klein_op_linear(x, a, h)
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    kb.klein_op_linear(x, a, h, ws)
+    kb.klein_op_linear(h, b, y, ws, residual=y, alpha=2.0)
+    assert kb.klein_sync()[0] == 0
+    ref = x.double() @ a.double().T
+    assert ((h.double() - ref).abs() <= SUM + (1e-5 + HALF[BF]) * ref.abs()).all()
+    z = h.double() @ b.double().T
+    ref = y0.double() + 2 * z
+    assert ((y.double() - ref).abs() <= 2 * (SUM + 1e-5 * z.abs()) + HALF[BF] * ref.abs() + 1e-7).all()
