@@ -1083,7 +1083,7 @@ static cudaError_t launch_rows_nb(const __nv_bfloat16* x, long long x_ld, const 
 // much re-reading of the weights. Measured on one B200 (us, back to back, against linear_gemm_kernel): 8 x 27648 x 3072
 // 29 (floor 26) against 50; 16 rows of it 33 against 38, 32 rows 54 against 39; 96 x 640 x 640 3.3 against 7.5;
 // 96 x 3072 x 1024 7.5 against 11, 96 x 3072 x 3072 19 against 13; 256 x 1024 x 256 5.1 against 6.3, 512 rows of it
-// 9.2 against 6.3; 4608 x 16 x 3072 5.6 against 13. At the border, operands not in L2: volume 9.0M (96 x 3072 x 1024) 7.5
+// 9.2 against 6.3; 4608 x 16 x 3072 5.6 against 13. At the border, four sets of operands in turn: volume 9.0M (96 x 3072 x 1024) 7.5
 // against 10.9, 10.0M (256 x 1024 x 1280) 9.4 against 10.0, 12.0M (64 x 3072 x 2048) 12.0 against 11.3, 13.5M
 // (4608 x 32 x 3072) 14.8 against 13.2, 16.0M (256 x 1024 x 2048) 14.2 against 10.5; columns fill the blocks of 16 worse
 // at 4608 x 24 x 3072 (10.1M), 14.5 against 13.2.
